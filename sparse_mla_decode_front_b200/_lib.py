@@ -100,6 +100,18 @@ SIGNATURES = {
     "mla_ipc_open": (ctypes.c_int, [ctypes.POINTER(MlaIpcHandle), ctypes.POINTER(ctypes.c_void_p)]),
     "mla_ipc_close": (ctypes.c_int, [_VP]),
 }
+_I, _F = ctypes.c_int, ctypes.c_float
+SIGNATURES.update({   # include/moe_experts.h
+    "mla_moe_sort_workspace_bytes": (ctypes.c_size_t, [_I] * 3),
+    "mla_moe_sort": (_I, [_VP] * 2 + [_I] * 6 + [_F] + [_VP] * 5 + [ctypes.c_size_t, _VP]),
+    "mla_moe_gather": (_I, [_VP, _I, _VP] + [_I] * 4 + [_VP] * 3),
+    "mla_moe_combine": (_I, [_VP, _I, _VP, _VP] + [_I] * 4 + [_VP] * 2),
+    "mla_moe_combine_backward": (_I, [_VP, _VP, _I, _VP, _VP] + [_I] * 4 + [_VP] * 3),
+    "mla_fp8_quantize": (_I, [_VP] + [_I] * 4 + [_VP] * 4),
+    "mla_fp8_matmul": (_I, [_VP] * 4 + [_I] * 3 + [_VP, _I, _VP, _VP]),
+    "mla_fp8_grouped_matmul": (_I, [_VP] * 5 + [_I] * 4 + [_VP, _I, _VP, _VP]),
+})
+MLA_DTYPE_BF16, MLA_DTYPE_FP16, MLA_DTYPE_FP32 = 0, 1, 2
 MLA_ROUTER_SIGMOID = 0
 MLA_ROUTER_SOFTMAX = 1
 

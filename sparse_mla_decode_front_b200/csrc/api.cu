@@ -138,13 +138,16 @@ int tp_table_of(const mla_tp_peers* tp, int hidden, int n_local, TpTable* t) {
 }
 
 }  // namespace
+
+bool cuda_call_failed(cudaError_t e) { return cuda_failed(e); }
+
 }  // namespace mla
 
 using namespace mla;
 
 extern "C" {
 
-int32_t mla_abi_version(void) { return (1 << 16) | 4; }
+int32_t mla_abi_version(void) { return (1 << 16) | 5; }
 
 const char* mla_status_string(int code) {
     switch (code) {

@@ -133,10 +133,11 @@ struct MapKey {
     const void* base;
     uint64_t inner, outer, row_bytes;
     uint32_t box_inner, box_outer;
-    int swizzle;
+    int swizzle, element_bytes;
     bool operator==(const MapKey& o) const {
         return base == o.base && inner == o.inner && outer == o.outer && row_bytes == o.row_bytes &&
-               box_inner == o.box_inner && box_outer == o.box_outer && swizzle == o.swizzle;
+               box_inner == o.box_inner && box_outer == o.box_outer && swizzle == o.swizzle &&
+               element_bytes == o.element_bytes;
     }
 };
 constexpr int kMapCache = 64;
@@ -154,8 +155,8 @@ MapCache& map_cache() {
 }  // namespace
 
 bool make_tma_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
-                 uint32_t box_inner, uint32_t box_outer, int swizzle_bytes) {
-    const MapKey k{base, inner, outer, row_bytes, box_inner, box_outer, swizzle_bytes};
+                 uint32_t box_inner, uint32_t box_outer, int swizzle_bytes, int element_bytes) {
+    const MapKey k{base, inner, outer, row_bytes, box_inner, box_outer, swizzle_bytes, element_bytes};
     MapCache& c = map_cache();
     {
         std::lock_guard<std::mutex> lock(c.mu);
@@ -171,7 +172,9 @@ bool make_tma_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t ou
     const cuuint64_t gstride[1] = {row_bytes};
     const cuuint32_t box[2] = {box_inner, box_outer};
     const cuuint32_t estride[2] = {1, 1};
-    if (fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), gdim, gstride, box, estride,
+    const CUtensorMapDataType type =
+        element_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (fn(map, type, 2, const_cast<void*>(base), gdim, gstride, box, estride,
            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return false;

@@ -101,9 +101,35 @@ cudaError_t launch_router_topk(const bf16* x, const bf16* gamma, const bf16* w, 
                                int K, float eps, int act, bf16* norm_out, int32_t* idx_out, bf16* aff_out,
                                void* workspace, cudaStream_t s, int* n_launches);
 
-// 2-D bf16 tensor map with a 128-byte (default) or 64-byte swizzle.
+// The routed experts (include/moe_experts.h; the dtype codes mirror MLA_DTYPE_*). Limits are
+// checked by the entry points.
+constexpr int kDtypeBf16 = 0, kDtypeFp16 = 1, kDtypeFp32 = 2;
+size_t moe_sort_workspace_bytes(int T, int K, int E);   // moe_sort.cu
+cudaError_t launch_moe_sort(const int32_t* idx, const bf16* aff, int T, int K, int n_total, int first, int E,
+                            int normalize, float scale, int32_t* offsets, int32_t* row_of, int32_t* source_of,
+                            float* weights, void* workspace, cudaStream_t s);
+bool moe_rows_fit(long long rows, int width);           // moe_rows.cu
+cudaError_t launch_moe_gather(const void* x, int dtype, const int32_t* row_of, int T, int K, int H, int R, void* rows,
+                              float* scales, cudaStream_t s);
+cudaError_t launch_moe_combine(const void* rows, int dtype, const int32_t* row_of, const float* w, int T, int K, int H,
+                               int R, void* out, cudaStream_t s);
+cudaError_t launch_moe_combine_backward(const void* dout, const void* rows, int dtype, const int32_t* row_of,
+                                        const float* w, int T, int K, int H, int R, void* drows, float* dw,
+                                        cudaStream_t s);
+cudaError_t launch_fp8_quantize(const void* x, int dtype, int R, int C, int gated, const int32_t* valid, void* q,
+                                float* scales, cudaStream_t s);
+bool fp8_gemm_fits(int rows, int groups, int n);        // fp8_gemm.cu
+cudaError_t launch_fp8_gemm(const void* x, const float* xs, const void* w, const float* ws, const int32_t* offsets,
+                            int rows, int groups, int n, int k, void* out, int dtype, int32_t* status, cudaStream_t s);
+
+// Remember a failed CUDA call of this host thread for mla_last_cuda_error_string (api.cu);
+// true if `e` is an error.
+bool cuda_call_failed(cudaError_t e);
+
+// 2-D tensor map of bf16 (element_bytes 2) or 8-bit values (1) with a 128-byte (default) or
+// 64-byte swizzle; inner and box_inner in elements.
 bool make_tma_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
-                 uint32_t box_inner, uint32_t box_outer, int swizzle_bytes = 128);
+                 uint32_t box_inner, uint32_t box_outer, int swizzle_bytes = 128, int element_bytes = 2);
 
 // Tensor-core attention core (core_tc.cu).
 constexpr int kCoreMaxClusters = 80;   // >= the 2-CTA clusters a B200 holds at once (148 SMs)

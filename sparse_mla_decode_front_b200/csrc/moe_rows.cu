@@ -1,0 +1,388 @@
+// Token rows to the experts' order and back, and rows quantised to e4m3
+// (include/moe_experts.h: mla_moe_gather, mla_moe_combine, mla_moe_combine_backward,
+// mla_fp8_quantize). All of them read and write each element once and do a few operations
+// on it, so they are bound by HBM at large sizes and by one chain of load latencies at small
+// ones. Rows are cut into units of 16 elements (every supported width is a multiple of 16),
+// one unit a thread, so a single token's row already spreads over several blocks and a
+// prompt's fills the GPU many times over.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace mla {
+namespace {
+
+constexpr int kUnit = 16;                         // elements a thread holds
+constexpr int kScaleBlock = 128;                  // elements that share a scale
+constexpr int kLanesPerScale = kScaleBlock / kUnit;
+constexpr int kThreads = 128;
+constexpr float kE4m3Max = 448.f;
+constexpr float kAmaxFloor = 7.888609052210118e-31f;   // 2^-100: 448 / amax stays finite, amax / 448 normal
+
+// ------------------------------------------------------------------ 16 elements <-> registers
+// Plain loads throughout, not the read-only path: a kernel may start before the one that
+// writes its inputs has ended (griddep_wait), and a load that the compiler takes for
+// invariant could be moved before that wait.
+template <class T>
+struct Unit;   // raw 16-byte words of 16 elements
+template <>
+struct Unit<float> {
+    static constexpr int kVecs = 4;
+    __device__ static float2 pair(const uint4* v, int i) { return reinterpret_cast<const float2*>(v)[i]; }
+    __device__ static void set(uint4* v, int i, float a, float b) { reinterpret_cast<float2*>(v)[i] = make_float2(a, b); }
+};
+template <>
+struct Unit<bf16> {
+    static constexpr int kVecs = 2;
+    __device__ static float2 pair(const uint4* v, int i) {
+        return __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(v)[i]);
+    }
+    __device__ static void set(uint4* v, int i, float a, float b) {
+        reinterpret_cast<__nv_bfloat162*>(v)[i] = __floats2bfloat162_rn(a, b);
+    }
+};
+template <>
+struct Unit<__half> {
+    static constexpr int kVecs = 2;
+    __device__ static float2 pair(const uint4* v, int i) { return __half22float2(reinterpret_cast<const __half2*>(v)[i]); }
+    __device__ static void set(uint4* v, int i, float a, float b) {
+        reinterpret_cast<__half2*>(v)[i] = __floats2half2_rn(a, b);
+    }
+};
+
+template <class T>
+__device__ __forceinline__ void load_unit(uint4* v, const T* p) {
+#pragma unroll
+    for (int i = 0; i < Unit<T>::kVecs; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+}
+template <class T>
+__device__ __forceinline__ void store_unit(T* p, const uint4* v) {
+#pragma unroll
+    for (int i = 0; i < Unit<T>::kVecs; ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
+}
+
+// Quantise the 128 values that the 8 lanes of a group hold (v: this lane's 16). The largest
+// magnitude is taken on the bit patterns, so a NaN (above infinity there) is not lost.
+__device__ __forceinline__ uint4 quantize_unit(const float (&v)[kUnit], float* scale) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = 1; o < kLanesPerScale; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float amax = __uint_as_float(max(m, __float_as_uint(kAmaxFloor)));
+    *scale = __fdiv_rn(amax, kE4m3Max);
+    const float inv = __fdiv_rn(kE4m3Max, amax);
+    uint4 q;
+    uint16_t* h = reinterpret_cast<uint16_t*>(&q);
+#pragma unroll
+    for (int i = 0; i < kUnit / 2; ++i)
+        h[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * inv, v[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    return q;
+}
+
+// ------------------------------------------------------------------ gather
+// One thread: one unit of one token, written to the token's rows. With FP8 a token is
+// quantised once, not once a copy; the lanes of a scale block past the row's end hold zeros.
+template <class T, bool FP8>
+__global__ void __launch_bounds__(kThreads)
+k_moe_gather(const T* x, const int32_t* row_of, int n_tokens, int K, int H, int R,
+             int units, void* rows, float* scales) {
+    griddep_launch();
+    griddep_wait();
+    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const long long t = id / units;
+    const int u = (int)(id - t * units);
+    const bool inside = t < n_tokens && u * kUnit < H;
+    if (!FP8 && !inside) return;
+    uint4 raw[Unit<T>::kVecs] = {};
+    if (inside) load_unit(raw, x + (size_t)t * H + u * kUnit);
+    int to[8];   // rows of the first choices, in flight with the unit
+#pragma unroll
+    for (int j = 0; j < 8; ++j) to[j] = inside && j < K ? row_of[t * K + j] : -1;
+    uint4 q = make_uint4(0, 0, 0, 0);
+    float scale = 0.f;
+    if (FP8) {
+        float v[kUnit];
+#pragma unroll
+        for (int i = 0; i < kUnit / 2; ++i) {
+            const float2 f = Unit<T>::pair(raw, i);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+        q = quantize_unit(v, &scale);
+        if (!inside) return;
+    }
+    for (int k0 = 0; k0 < K; k0 += 8) {
+        if (k0 > 0)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) to[j] = k0 + j < K ? row_of[t * K + k0 + j] : -1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = to[j];
+            if ((unsigned)r >= (unsigned)R) continue;
+            if (FP8) {
+                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(rows) + (size_t)r * H + u * kUnit) = q;
+                if (u % kLanesPerScale == 0) scales[(size_t)(u / kLanesPerScale) * R + r] = scale;
+            } else {
+                store_unit(static_cast<T*>(rows) + (size_t)r * H + u * kUnit, raw);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ combine
+// One thread: one unit of one token's output; the rows of kBatch choices are in flight at once.
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+k_moe_combine(const T* rows, const int32_t* row_of, const float* weights,
+              int n_tokens, int K, int H, int R, int units, T* out) {
+    constexpr int kBatch = 4;
+    griddep_launch();
+    griddep_wait();
+    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const long long t = id / units;
+    const int u = (int)(id - t * units);
+    if (t >= n_tokens) return;
+    float acc[kUnit] = {};
+    for (int k0 = 0; k0 < K; k0 += kBatch) {
+        uint4 raw[kBatch][Unit<T>::kVecs];
+        float w[kBatch];
+        bool on[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int r = k0 + j < K ? row_of[t * K + k0 + j] : -1;
+            on[j] = (unsigned)r < (unsigned)R;
+            w[j] = 1.f;
+            if (on[j]) {
+                if (weights) w[j] = weights[t * K + k0 + j];
+                load_unit(raw[j], rows + (size_t)r * H + u * kUnit);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (!on[j]) continue;
+#pragma unroll
+            for (int i = 0; i < kUnit / 2; ++i) {
+                const float2 f = Unit<T>::pair(raw[j], i);
+                acc[2 * i] = fmaf(w[j], f.x, acc[2 * i]);
+                acc[2 * i + 1] = fmaf(w[j], f.y, acc[2 * i + 1]);
+            }
+        }
+    }
+    uint4 o[Unit<T>::kVecs];
+#pragma unroll
+    for (int i = 0; i < kUnit / 2; ++i) Unit<T>::set(o, i, acc[2 * i], acc[2 * i + 1]);
+    store_unit(out + (size_t)t * H + u * kUnit, o);
+}
+
+// ------------------------------------------------------------------ combine, backward
+// A team of `team` warps takes one choice: grad_row = w grad_out[t], and the dot product of
+// grad_out[t] with the row. Blocks of 8 warps hold 8 / team neighbouring choices, so the
+// choices of a token read its grad_out from L1 / L2. Few choices: 8 warps each, for latency;
+// many: one.
+constexpr int kBackWarps = 8;
+template <class T>
+__global__ void __launch_bounds__(32 * kBackWarps)
+k_moe_combine_backward(const T* dout, const T* rows, const int32_t* row_of,
+                       const float* weights, long long n, int K, int H, int R, int units, int team,
+                       T* drows, float* dw) {
+    __shared__ float part[kBackWarps];
+    griddep_launch();
+    griddep_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int member = warp % team;
+    const long long c = (long long)blockIdx.x * (kBackWarps / team) + warp / team;   // choice t * K + k
+    const int r = c < n ? row_of[c] : -1;
+    float sum = 0.f;
+    if ((unsigned)r < (unsigned)R) {
+        const float w = weights ? weights[c] : 1.f;
+        const T* d = dout + (size_t)(c / K) * H;
+        const T* x = rows + (size_t)r * H;
+        T* g = drows + (size_t)r * H;
+        constexpr int kBatch = 2;   // units in flight
+        for (int u0 = member * 32 + lane; u0 < units; u0 += 32 * team * kBatch) {
+            uint4 rd[kBatch][Unit<T>::kVecs], rx[kBatch][Unit<T>::kVecs], ro[Unit<T>::kVecs];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int u = u0 + b * 32 * team;
+                if (u >= units) break;
+                load_unit(rd[b], d + u * kUnit);
+                if (dw) load_unit(rx[b], x + u * kUnit);
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int u = u0 + b * 32 * team;
+                if (u >= units) break;
+                if (dw) {
+                    float s = 0.f;
+#pragma unroll
+                    for (int i = 0; i < kUnit / 2; ++i) {
+                        const float2 p = Unit<T>::pair(rd[b], i), v = Unit<T>::pair(rx[b], i);
+                        s = fmaf(p.x, v.x, s);
+                        s = fmaf(p.y, v.y, s);
+                    }
+                    sum += s;
+                }
+                if (drows) {
+#pragma unroll
+                    for (int i = 0; i < kUnit / 2; ++i) {
+                        const float2 p = Unit<T>::pair(rd[b], i);
+                        Unit<T>::set(ro, i, w * p.x, w * p.y);
+                    }
+                    store_unit(g + u * kUnit, ro);
+                }
+            }
+        }
+    }
+    if (!dw) return;
+    sum = warp_sum(sum);
+    if (team == 1) {
+        if (lane == 0 && c < n) dw[c] = sum;
+        return;
+    }
+    if (lane == 0) part[warp] = sum;
+    __syncthreads();
+    if (member == 0 && lane == 0 && c < n) {
+        float s = 0.f;
+        for (int i = 0; i < team; ++i) s += part[warp + i];   // a fixed order
+        dw[c] = s;
+    }
+}
+
+// ------------------------------------------------------------------ quantise
+// One thread: one unit of one row. The gated activation in fp32: exp and the division by the
+// fast forms (2 ulp and exp's 2 + |1.16 g| ulp), far below e4m3's 2^-4.
+template <class T, bool GATED>
+__global__ void __launch_bounds__(kThreads)
+k_fp8_quantize(const T* x, int R, int C, int units, const int32_t* valid_rows,
+               uint8_t* q, float* scales) {
+    griddep_launch();
+    griddep_wait();
+    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const long long r = id / units;
+    const int u = (int)(id - r * units);
+    const int rows = valid_rows ? min(R, *valid_rows) : R;
+    const bool inside = r < rows && u * kUnit < C;
+    uint4 rg[Unit<T>::kVecs] = {}, ru[Unit<T>::kVecs] = {};
+    if (inside) {
+        const T* p = x + (size_t)r * (GATED ? 2 * C : C) + u * kUnit;
+        load_unit(rg, p);
+        if (GATED) load_unit(ru, p + C);
+    }
+    float v[kUnit];
+#pragma unroll
+    for (int i = 0; i < kUnit / 2; ++i) {
+        float2 g = Unit<T>::pair(rg, i);
+        if (GATED) {
+            const float2 m = Unit<T>::pair(ru, i);
+            g.x = __fdividef(g.x, 1.f + __expf(-g.x)) * m.x;
+            g.y = __fdividef(g.y, 1.f + __expf(-g.y)) * m.y;
+        }
+        v[2 * i] = g.x;
+        v[2 * i + 1] = g.y;
+    }
+    float scale;
+    const uint4 o = quantize_unit(v, &scale);
+    if (!inside) return;
+    *reinterpret_cast<uint4*>(q + (size_t)r * C + u * kUnit) = o;
+    if (u % kLanesPerScale == 0) scales[(size_t)(u / kLanesPerScale) * R + r] = scale;
+}
+
+// Units of a row: whole scale blocks when lanes share a scale, else the row's own.
+int row_units(int width, bool whole_blocks) {
+    return whole_blocks ? (width + kScaleBlock - 1) / kScaleBlock * kLanesPerScale : width / kUnit;
+}
+unsigned blocks_for(long long rows, int units) { return (unsigned)((rows * units + kThreads - 1) / kThreads); }
+
+template <class T>
+cudaError_t gather_as(const void* x, const int32_t* row_of, int T_, int K, int H, int R, void* rows, float* scales,
+                      cudaStream_t s) {
+    const int units = row_units(H, scales != nullptr);
+    const dim3 grid(blocks_for(T_, units));
+    const T* xt = static_cast<const T*>(x);
+    if (scales)
+        return launch_pdl(k_moe_gather<T, true>, grid, dim3(kThreads), 0, s, xt, row_of, T_, K, H, R, units, rows, scales);
+    return launch_pdl(k_moe_gather<T, false>, grid, dim3(kThreads), 0, s, xt, row_of, T_, K, H, R, units, rows, scales);
+}
+
+template <class T>
+cudaError_t combine_as(const void* rows, const int32_t* row_of, const float* w, int T_, int K, int H, int R, void* out,
+                       cudaStream_t s) {
+    const int units = row_units(H, false);
+    return launch_pdl(k_moe_combine<T>, dim3(blocks_for(T_, units)), dim3(kThreads), 0, s,
+                      static_cast<const T*>(rows), row_of, w, T_, K, H, R, units, static_cast<T*>(out));
+}
+
+template <class T>
+cudaError_t combine_backward_as(const void* dout, const void* rows, const int32_t* row_of, const float* w, int T_,
+                                int K, int H, int R, void* drows, float* dw, cudaStream_t s) {
+    const long long n = (long long)T_ * K;
+    const int units = row_units(H, false);
+    const int team = n < 592 ? 8 : 1;
+    const long long per_block = kBackWarps / team;
+    return launch_pdl(k_moe_combine_backward<T>, dim3((unsigned)((n + per_block - 1) / per_block)),
+                      dim3(32 * kBackWarps), 0, s, static_cast<const T*>(dout), static_cast<const T*>(rows), row_of, w,
+                      n, K, H, R, units, team, static_cast<T*>(drows), dw);
+}
+
+template <class T>
+cudaError_t quantize_as(const void* x, int R, int C, int gated, const int32_t* valid, void* q, float* scales,
+                        cudaStream_t s) {
+    const int units = row_units(C, true);
+    const dim3 grid(blocks_for(R, units));
+    const T* xt = static_cast<const T*>(x);
+    uint8_t* qt = static_cast<uint8_t*>(q);
+    if (gated)
+        return launch_pdl(k_fp8_quantize<T, true>, grid, dim3(kThreads), 0, s, xt, R, C, units, valid, qt, scales);
+    return launch_pdl(k_fp8_quantize<T, false>, grid, dim3(kThreads), 0, s, xt, R, C, units, valid, qt, scales);
+}
+
+}  // namespace
+
+// Blocks of 128 threads over rows x units: the grid's x extent holds 2^31 - 1.
+bool moe_rows_fit(long long rows, int width) {
+    return (rows * row_units(width, true) + kThreads - 1) / kThreads < (1LL << 31);
+}
+
+cudaError_t launch_moe_gather(const void* x, int dtype, const int32_t* row_of, int T, int K, int H, int R, void* rows,
+                              float* scales, cudaStream_t s) {
+    switch (dtype) {
+        case kDtypeBf16: return gather_as<bf16>(x, row_of, T, K, H, R, rows, scales, s);
+        case kDtypeFp16: return gather_as<__half>(x, row_of, T, K, H, R, rows, scales, s);
+        default: return gather_as<float>(x, row_of, T, K, H, R, rows, scales, s);
+    }
+}
+
+cudaError_t launch_moe_combine(const void* rows, int dtype, const int32_t* row_of, const float* w, int T, int K, int H,
+                               int R, void* out, cudaStream_t s) {
+    switch (dtype) {
+        case kDtypeBf16: return combine_as<bf16>(rows, row_of, w, T, K, H, R, out, s);
+        case kDtypeFp16: return combine_as<__half>(rows, row_of, w, T, K, H, R, out, s);
+        default: return combine_as<float>(rows, row_of, w, T, K, H, R, out, s);
+    }
+}
+
+cudaError_t launch_moe_combine_backward(const void* dout, const void* rows, int dtype, const int32_t* row_of,
+                                        const float* w, int T, int K, int H, int R, void* drows, float* dw,
+                                        cudaStream_t s) {
+    switch (dtype) {
+        case kDtypeBf16: return combine_backward_as<bf16>(dout, rows, row_of, w, T, K, H, R, drows, dw, s);
+        case kDtypeFp16: return combine_backward_as<__half>(dout, rows, row_of, w, T, K, H, R, drows, dw, s);
+        default: return combine_backward_as<float>(dout, rows, row_of, w, T, K, H, R, drows, dw, s);
+    }
+}
+
+cudaError_t launch_fp8_quantize(const void* x, int dtype, int R, int C, int gated, const int32_t* valid, void* q,
+                                float* scales, cudaStream_t s) {
+    switch (dtype) {
+        case kDtypeBf16: return quantize_as<bf16>(x, R, C, gated, valid, q, scales, s);
+        case kDtypeFp16: return quantize_as<__half>(x, R, C, gated, valid, q, scales, s);
+        default: return quantize_as<float>(x, R, C, gated, valid, q, scales, s);
+    }
+}
+
+}  // namespace mla

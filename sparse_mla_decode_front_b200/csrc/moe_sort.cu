@@ -1,0 +1,303 @@
+// The router's choices sorted by expert (include/moe_experts.h, mla_moe_sort): a stable
+// counting sort over E + 1 bins (the held experts, and one for choices without a row here).
+//
+// With key(i) the bin of choice i (token-major), row(i) = #{j : key(j) < key(i)} +
+// #{j < i : key(j) = key(i)}. Each warp takes a run of consecutive choices, 32 at a time:
+// equal keys of a group of 32 are found with one match, the choice's place among them is a
+// population count, and the warp's own bin counts (shared memory) carry the place from one
+// group to the next. The counts are then summed over the warps before, bin by bin. No
+// atomics decide a place, so the order is that of the choices.
+//
+// The data is a few bytes a choice; what costs is the chain of latencies and the launches.
+// Up to kSingleItems choices run in one launch, one block for the sort and further blocks
+// for the routing weights beside it; more are cut into chunks, a first launch counting each
+// chunk's bins and a second placing the chunk behind the chunks before it.
+#include <algorithm>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace mla {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kPerLane = 4;                            // choices a lane holds in one pass
+constexpr int kPassItems = kThreads * kPerLane;        // choices of one pass of a block
+constexpr int kSingleItems = kPassItems;
+constexpr int kMaxChunks = 256;                        // chunks (blocks) of the two-launch form
+constexpr int kWeightTokens = kThreads;                // tokens of one weight block
+constexpr unsigned kAll = 0xffffffffu;
+
+struct Args {
+    const int32_t* idx;
+    const bf16* aff;
+    int T, K, n_total, first, E, normalize;
+    float scale;
+    int32_t *offsets, *row_of, *source_of;
+    float* weights;
+    int32_t* hist;        // [chunks][E + 1] of the two-launch form
+    int n, chunks, chunk_items;
+};
+
+__device__ __forceinline__ int key_of(const Args& a, int i) {
+    const int e = a.idx[i] - a.first;
+    return (unsigned)e < (unsigned)a.E ? e : a.E;
+}
+
+// Routing weights of the tokens of block `b` of the weight blocks, one token a thread.
+__device__ void token_weights(const Args& a, int b) {
+    const int t = b * kWeightTokens + threadIdx.x;
+    if (t >= a.T) return;
+    const int32_t* idx = a.idx + (size_t)t * a.K;
+    const bf16* aff = a.aff + (size_t)t * a.n_total;
+    float v[8];
+    float sum = 0.f;
+    for (int k0 = 0; k0 < a.K; k0 += 8) {   // eight loads in flight
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int e = k0 + j < a.K ? idx[k0 + j] : -1;
+            v[j] = (unsigned)e < (unsigned)a.n_total ? bf2f(aff[e]) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += v[j];
+    }
+    for (int k0 = 0; k0 < a.K; k0 += 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (k0 + j >= a.K) break;
+            if (a.K > 8) {   // more than one group: read again (cached)
+                const int e = idx[k0 + j];
+                v[j] = (unsigned)e < (unsigned)a.n_total ? bf2f(aff[e]) : 0.f;
+            }
+            const float w = !a.normalize ? v[j] : sum == 0.f ? 0.f : v[j] / sum;
+            a.weights[(size_t)t * a.K + k0 + j] = a.scale * w;
+        }
+    }
+}
+
+// Exclusive prefix sum of v over the block's threads; `red` holds kWarps ints.
+__device__ int block_exclusive(int v, int* red) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kAll, s, o);
+        if (lane >= o) s += u;
+    }
+    if (lane == 31) red[wid] = s;
+    __syncthreads();
+    if (wid == 0) {
+        int r = red[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(kAll, r, o);
+            if (lane >= o) r += u;
+        }
+        red[lane] = r;
+    }
+    __syncthreads();
+    const int before = wid ? red[wid - 1] : 0;
+    __syncthreads();
+    return before + s - v;
+}
+
+// Exclusive prefix over the E + 1 bins of total[] into base[] (both in shared memory).
+__device__ void bin_bases(const int* total, int* base, int bins, int* red) {
+    int carry = 0;
+    for (int b0 = 0; b0 < bins; b0 += kThreads) {   // one trip up to 1024 bins, a second for bin 1024
+        const int b = b0 + threadIdx.x;
+        const int v = b < bins ? total[b] : 0;
+        const int ex = block_exclusive(v, red);
+        if (b < bins) base[b] = carry + ex;
+        __shared__ int last;
+        if (threadIdx.x == kThreads - 1) last = ex + v;
+        __syncthreads();
+        carry += last;
+        __syncthreads();
+    }
+}
+
+// Place up to kPassItems choices [i0, i1): base[] holds each bin's next row and is advanced.
+// `single`: base[] is computed here from this pass's own counts (the whole input), and the
+// offsets are written. cnt: [kWarps][bins] uint16 counts, total / base: [bins].
+__device__ void place_pass(const Args& a, int i0, int i1, uint16_t* cnt, int* total, int* base, int* red,
+                           bool single) {
+    const int bins = a.E + 1, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    int key[kPerLane], place[kPerLane];
+    const int w0 = i0 + wid * (32 * kPerLane);
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+        const int i = w0 + 32 * j + lane;
+        key[j] = i < i1 ? key_of(a, i) : -1;
+    }
+    uint32_t* cw = reinterpret_cast<uint32_t*>(cnt);
+    for (int b = threadIdx.x; b < (kWarps * bins + 1) / 2; b += kThreads) cw[b] = 0;
+    __syncthreads();
+    uint16_t* mine = cnt + wid * bins;
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+        const unsigned same = __match_any_sync(kAll, key[j]);
+        const unsigned before = same & ((1u << lane) - 1);
+        place[j] = 0;
+        if (key[j] >= 0) place[j] = mine[key[j]] + __popc(before);
+        __syncwarp();
+        if (key[j] >= 0 && before == 0) mine[key[j]] += (uint16_t)__popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    // counts -> counts of the warps before; a bin's sum over all warps to total[]
+    for (int b = threadIdx.x; b < bins; b += kThreads) {
+        int s = 0;
+#pragma unroll 8
+        for (int w = 0; w < kWarps; ++w) {
+            const int c = cnt[w * bins + b];
+            cnt[w * bins + b] = (uint16_t)s;
+            s += c;
+        }
+        total[b] = s;
+    }
+    __syncthreads();
+    if (single) {
+        bin_bases(total, base, bins, red);
+        for (int b = threadIdx.x; b < bins; b += kThreads) a.offsets[b] = base[b];
+    }
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+        if (key[j] < 0) continue;
+        const int i = w0 + 32 * j + lane;
+        const int row = base[key[j]] + mine[key[j]] + place[j];
+        const bool here = key[j] < a.E;
+        a.row_of[i] = here ? row : -1;
+        a.source_of[row] = here ? i : -1;   // the last bin's rows lie behind the last expert's
+    }
+    if (!single) {
+        __syncthreads();
+        for (int b = threadIdx.x; b < bins; b += kThreads) base[b] += total[b];
+        __syncthreads();
+    }
+}
+
+// Shared memory: total and base [bins], then the warps' counts.
+size_t smem_bytes(int bins) { return sizeof(int) * 2 * bins + sizeof(uint16_t) * (kWarps * bins + 1) + 4; }
+
+__global__ void __launch_bounds__(kThreads) k_moe_sort_single(Args a) {
+    extern __shared__ int sm[];
+    __shared__ int red[kWarps];
+    griddep_launch();
+    griddep_wait();
+    if (blockIdx.x > 0) {
+        token_weights(a, blockIdx.x - 1);
+        return;
+    }
+    const int bins = a.E + 1;
+    place_pass(a, 0, a.n, reinterpret_cast<uint16_t*>(sm + 2 * bins), sm, sm + bins, red, true);
+}
+
+// First launch: blocks [0, chunks) count their chunk's bins, the others weigh tokens.
+__global__ void __launch_bounds__(kThreads) k_moe_sort_count(Args a) {
+    extern __shared__ int sm[];
+    griddep_launch();
+    griddep_wait();
+    if ((int)blockIdx.x >= a.chunks) {
+        token_weights(a, blockIdx.x - a.chunks);
+        return;
+    }
+    const int bins = a.E + 1;
+    for (int b = threadIdx.x; b < bins; b += kThreads) sm[b] = 0;
+    __syncthreads();
+    const int i0 = blockIdx.x * a.chunk_items;                   // < n, so no overflow
+    const int len = min(a.chunk_items, a.n - i0);
+    for (int i = threadIdx.x; i < len; i += kThreads) atomicAdd(sm + key_of(a, i0 + i), 1);   // whole numbers: any order
+    __syncthreads();
+    for (int b = threadIdx.x; b < bins; b += kThreads) a.hist[(size_t)blockIdx.x * bins + b] = sm[b];
+}
+
+// Second launch: each block's bases are the bins before plus the same bin of the chunks before.
+__global__ void __launch_bounds__(kThreads) k_moe_sort_place(Args a) {
+    extern __shared__ int sm[];
+    __shared__ int red[kWarps];
+    griddep_launch();
+    griddep_wait();
+    const int bins = a.E + 1;
+    int *total = sm, *base = sm + bins;
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(sm + 2 * bins);
+    int* before = reinterpret_cast<int*>(cnt);   // [bins], until the first pass
+    for (int b = threadIdx.x; b < bins; b += kThreads) total[b] = before[b] = 0;
+    __syncthreads();
+    // several threads share a bin where there are few bins
+    const int teams = max(1, kThreads / bins);
+    const int team = threadIdx.x / bins, b1 = threadIdx.x - team * bins;
+    for (int b = bins <= kThreads ? (team < teams ? b1 : bins) : threadIdx.x; b < bins;
+         b += bins <= kThreads ? bins : kThreads) {
+        int all = 0, prev = 0;
+        const int t0 = bins <= kThreads ? team : 0, step = bins <= kThreads ? teams : 1;
+#pragma unroll 4
+        for (int c = t0; c < a.chunks; c += step) {
+            const int h = __ldcg(a.hist + (size_t)c * bins + b);
+            all += h;
+            prev += c < (int)blockIdx.x ? h : 0;
+        }
+        atomicAdd(total + b, all);
+        atomicAdd(before + b, prev);
+    }
+    __syncthreads();
+    bin_bases(total, base, bins, red);
+    if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b < bins; b += kThreads) a.offsets[b] = base[b];
+    __syncthreads();
+    for (int b = threadIdx.x; b < bins; b += kThreads) base[b] += before[b];
+    __syncthreads();
+    const int c0 = blockIdx.x * a.chunk_items;
+    const int len = min(a.chunk_items, a.n - c0);
+    for (int o = 0; o < len; o += kPassItems)
+        place_pass(a, c0 + o, c0 + min(len, o + kPassItems), cnt, total, base, red, false);
+}
+
+// Chunks of whole passes, at most kMaxChunks of them.
+void chunking(long long n, int* chunks, int* items) {
+    const long long passes = (n + kPassItems - 1) / kPassItems;
+    const long long per = (passes + kMaxChunks - 1) / kMaxChunks;
+    *items = (int)std::min<long long>(per * kPassItems, 1LL << 30);
+    *chunks = (int)((n + *items - 1) / *items);
+}
+
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+    return bytes > 48 * 1024
+               ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
+               : cudaSuccess;
+}
+
+}  // namespace
+
+size_t moe_sort_workspace_bytes(int T, int K, int E) {
+    const long long n = (long long)T * K;
+    if (n <= kSingleItems) return 0;
+    int chunks, items;
+    chunking(n, &chunks, &items);
+    return sizeof(int32_t) * (size_t)chunks * (E + 1);
+}
+
+cudaError_t launch_moe_sort(const int32_t* idx, const bf16* aff, int T, int K, int n_total, int first, int E,
+                            int normalize, float scale, int32_t* offsets, int32_t* row_of, int32_t* source_of,
+                            float* weights, void* workspace, cudaStream_t s) {
+    if (T == 0) return cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (E + 1), s);
+    Args a{idx, aff, T, K, n_total, first, E, normalize, scale, offsets, row_of, source_of, weights,
+           static_cast<int32_t*>(workspace), T * K, 1, 0};
+    const int weight_blocks = aff ? (T + kWeightTokens - 1) / kWeightTokens : 0;
+    const size_t smem = smem_bytes(E + 1);
+    if (a.n <= kSingleItems) {
+        cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_moe_sort_single), smem);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(k_moe_sort_single, dim3(1 + weight_blocks), dim3(kThreads), smem, s, a);
+    }
+    chunking(a.n, &a.chunks, &a.chunk_items);
+    cudaError_t e = launch_pdl(k_moe_sort_count, dim3(a.chunks + weight_blocks), dim3(kThreads),
+                               sizeof(int) * (E + 1), s, a);
+    if (e != cudaSuccess) return e;
+    e = allow_smem(reinterpret_cast<const void*>(k_moe_sort_place), smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k_moe_sort_place, dim3(a.chunks), dim3(kThreads), smem, s, a);
+}
+
+}  // namespace mla

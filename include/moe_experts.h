@@ -29,8 +29,8 @@
  * captured into a CUDA graph.
  *
  * Buffers must not overlap. Row indices and offsets are read on the device: a row index
- * outside [0, R) counts as no row, and offsets are clamped to [0, R], so that a wrong table
- * gives wrong values but never an access out of bounds.
+ * outside [0, R) counts as no row, and offsets are clamped to [0, R] and to their running
+ * maximum, so that a wrong table gives wrong values but never an access out of bounds.
  */
 #ifndef MOE_EXPERTS_H
 #define MOE_EXPERTS_H

@@ -17,6 +17,15 @@ int sms_of(int dev) {
     return n;
 }
 
+// Shared memory of `kern` raised to `bytes`, once per kernel (its flags `set`) and device.
+template <class K>
+cudaError_t allow_smem(K kern, int bytes, bool* set, int dev) {
+    if (dev >= 0 && dev < kMaxDevices && set[dev]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) set[dev] = true;
+    return e;
+}
+
 template <int BN>
 cudaError_t launch_few(const void* x, const void* w, const fp8::Problem& p, cudaStream_t s) {
     using C = fp8::FewCfg<BN>;
@@ -24,12 +33,9 @@ cudaError_t launch_few(const void* x, const void* w, const fp8::Problem& p, cuda
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    static bool attr_set[kMaxDevices] = {};   // per instantiation and device
-    if (dev < 0 || dev >= kMaxDevices || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < kMaxDevices) attr_set[dev] = true;
-    }
+    static bool attr_set[kMaxDevices] = {};
+    e = allow_smem(kern, C::kSmem, attr_set, dev);
+    if (e != cudaSuccess) return e;
     CUtensorMap tw, tx;
     if (!make_tma_2d(&tw, w, (uint64_t)p.k, (uint64_t)p.groups * p.n, (uint64_t)p.k, fp8::BK, fp8::BF, 128, 1) ||
         !make_tma_2d(&tx, x, (uint64_t)p.k, (uint64_t)p.rows, (uint64_t)p.k, fp8::BK, BN, 128, 1))
@@ -37,6 +43,42 @@ cudaError_t launch_few(const void* x, const void* w, const fp8::Problem& p, cuda
     const long long tiles = ((long long)(p.rows + BN - 1) / BN + p.groups - 1) * ((p.n + fp8::BF - 1) / fp8::BF);
     const int grid = (int)std::min<long long>(tiles, sms_of(dev));
     return launch_pdl(kern, dim3(grid), dim3(fp8::kFewThreads), C::kSmem, s, tw, tx, p);
+}
+
+// Width of k_fp8_many's tiles: the one whose last wave costs least. A wave takes bn tensor
+// columns (and a little that does not depend on bn) per K block on every SM.
+int many_bn(long long row_tiles, int n, int sms) {
+    int best = 256;
+    long long best_cost = -1;
+    for (int bn = 256; bn >= 64; bn -= 32) {
+        const long long tiles = row_tiles * ((n + bn - 1) / bn);
+        const long long cost = (tiles + sms - 1) / sms * (bn + 32);
+        if (best_cost < 0 || cost < best_cost) {
+            best_cost = cost;
+            best = bn;
+        }
+    }
+    return best;
+}
+
+cudaError_t launch_many(const void* x, const void* w, const fp8::Problem& p, cudaStream_t s) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static bool attr_set[kMaxDevices] = {};
+    e = allow_smem(fp8::k_fp8_many, fp8::kManySmem, attr_set, dev);
+    if (e != cudaSuccess) return e;
+    // a group's last row tile is half empty on average
+    const long long row_tiles = ((long long)p.rows + fp8::kManyRows - 1) / fp8::kManyRows + (p.groups - 1) / 2;
+    const int bn = many_bn(row_tiles, p.n, sms_of(dev));
+    CUtensorMap tx, tw;
+    if (!make_tma_2d(&tx, x, (uint64_t)p.k, (uint64_t)p.rows, (uint64_t)p.k, fp8::BK, fp8::kManyRows, 128, 1) ||
+        !make_tma_2d(&tw, w, (uint64_t)p.k, (uint64_t)p.groups * p.n, (uint64_t)p.k, fp8::BK, bn, 128, 1))
+        return cudaErrorInvalidValue;
+    const long long tiles =
+        (((long long)p.rows + fp8::kManyRows - 1) / fp8::kManyRows + p.groups - 1) * ((p.n + bn - 1) / bn);
+    const int grid = (int)std::min<long long>(tiles, sms_of(dev));
+    return launch_pdl(fp8::k_fp8_many, dim3(grid), dim3(fp8::kManyThreads), fp8::kManySmem, s, tx, tw, p, bn);
 }
 
 }  // namespace
@@ -54,7 +96,8 @@ cudaError_t launch_fp8_gemm(const void* x, const float* xs, const void* w, const
     if (per_group <= 16) return launch_few<16>(x, w, p, s);
     if (per_group <= 32) return launch_few<32>(x, w, p, s);
     if (per_group <= 64) return launch_few<64>(x, w, p, s);
-    return launch_few<128>(x, w, p, s);
+    if (per_group <= 128) return launch_few<128>(x, w, p, s);
+    return launch_many(x, w, p, s);
 }
 
 }  // namespace mla

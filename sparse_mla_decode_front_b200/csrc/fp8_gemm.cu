@@ -45,22 +45,6 @@ cudaError_t launch_few(const void* x, const void* w, const fp8::Problem& p, cuda
     return launch_pdl(kern, dim3(grid), dim3(fp8::kFewThreads), C::kSmem, s, tw, tx, p);
 }
 
-// Width of k_fp8_many's tiles: the one whose last wave costs least. A wave takes bn tensor
-// columns (and a little that does not depend on bn) per K block on every SM.
-int many_bn(long long row_tiles, int n, int sms) {
-    int best = 256;
-    long long best_cost = -1;
-    for (int bn = 256; bn >= 64; bn -= 32) {
-        const long long tiles = row_tiles * ((n + bn - 1) / bn);
-        const long long cost = (tiles + sms - 1) / sms * (bn + 32);
-        if (best_cost < 0 || cost < best_cost) {
-            best_cost = cost;
-            best = bn;
-        }
-    }
-    return best;
-}
-
 cudaError_t launch_many(const void* x, const void* w, const fp8::Problem& p, cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -68,17 +52,15 @@ cudaError_t launch_many(const void* x, const void* w, const fp8::Problem& p, cud
     static bool attr_set[kMaxDevices] = {};
     e = allow_smem(fp8::k_fp8_many, fp8::kManySmem, attr_set, dev);
     if (e != cudaSuccess) return e;
-    // a group's last row tile is half empty on average
-    const long long row_tiles = ((long long)p.rows + fp8::kManyRows - 1) / fp8::kManyRows + (p.groups - 1) / 2;
-    const int bn = many_bn(row_tiles, p.n, sms_of(dev));
     CUtensorMap tx, tw;
     if (!make_tma_2d(&tx, x, (uint64_t)p.k, (uint64_t)p.rows, (uint64_t)p.k, fp8::BK, fp8::kManyRows, 128, 1) ||
-        !make_tma_2d(&tw, w, (uint64_t)p.k, (uint64_t)p.groups * p.n, (uint64_t)p.k, fp8::BK, bn, 128, 1))
+        !make_tma_2d(&tw, w, (uint64_t)p.k, (uint64_t)p.groups * p.n, (uint64_t)p.k, fp8::BK, fp8::kManyFeatures / 2, 128, 1))
         return cudaErrorInvalidValue;
-    const long long tiles =
-        (((long long)p.rows + fp8::kManyRows - 1) / fp8::kManyRows + p.groups - 1) * ((p.n + bn - 1) / bn);
-    const int grid = (int)std::min<long long>(tiles, sms_of(dev));
-    return launch_pdl(fp8::k_fp8_many, dim3(grid), dim3(fp8::kManyThreads), fp8::kManySmem, s, tx, tw, p, bn);
+    const int rows = 2 * fp8::kManyRows;
+    const long long tiles = (((long long)p.rows + rows - 1) / rows + p.groups - 1) *
+                            ((p.n + fp8::kManyFeatures - 1) / fp8::kManyFeatures);
+    const int pairs = (int)std::min<long long>(tiles, std::max(1, sms_of(dev) / 2));
+    return launch_pdl(fp8::k_fp8_many, dim3(2 * pairs), dim3(fp8::kManyThreads), fp8::kManySmem, s, tx, tw, p);
 }
 
 }  // namespace

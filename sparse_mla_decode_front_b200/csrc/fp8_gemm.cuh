@@ -34,7 +34,9 @@ constexpr int BF = 128;          // features per tile = UMMA M
 constexpr int BK = 128;          // K block = scale block = one 128-byte swizzle atom
 constexpr int kBufs = 4;         // accumulators in TMEM
 constexpr int kMaxGroups = 1024;
-constexpr int kFewThreads = 224;
+constexpr int kFewThreads = 256;
+constexpr int kScales = 8;        // K blocks whose scales are handed over at once
+constexpr int kFewIssuer2 = 7;    // warp of the second issuer
 
 struct Problem {
     const float *xs, *ws;        // x_scales [kb][rows], w_scales [groups][nb][kb]
@@ -121,6 +123,39 @@ __device__ __forceinline__ Tile tile_at(const Groups& G, int groups, int t, int 
     return Tile{lo, G.bound[lo] + rt * rows_per_tile, rows - rt * rows_per_tile, ft * bf};
 }
 
+// Tiles of this CTA.
+__device__ __forceinline__ int my_tiles(int tiles) {
+    return (int)blockIdx.x < tiles ? (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+}
+
+// The UMMAs of every second K block of the CTA, from block `first` on; total: all its tiles'
+// blocks. One thread needs about 870 clocks a block (two waits of about 120, four UMMAs, two
+// commits of about 75, each of which it sits out; measured on the 128 x 256 tile), more than
+// the 512 that the tensor cores need. The blocks' accumulators are independent, so two
+// threads of different warps take turns: 1.4 to 2 times the rate. `issue(stage, buf)` issues
+// one block's. Past K both operands are zero-filled, so a partial last block has no other form.
+template <int S, int BUFS, class F>
+__device__ __forceinline__ bool issue_blocks(int first, long long total, uint64_t* full_bar, uint64_t* empty_bar,
+                                             uint64_t* acc_full, uint64_t* acc_empty, int32_t* status, F issue) {
+    static_assert(S >= 2 && BUFS % 2 == 0, "each issuer has its own accumulators");
+    int stage = first, buf = first;
+    uint32_t phase = 0, buf_phase = 0;
+    for (long long i = first; i < total; i += 2) {
+        if (!ptx::mbar_wait(&full_bar[stage], phase, status) ||
+            !ptx::mbar_wait(&acc_empty[buf], buf_phase ^ 1, status))
+            return false;
+        ptx::tc_fence_after();
+        issue(stage, buf);
+        ptx::umma_commit(&acc_full[buf]);
+        ptx::umma_commit(&empty_bar[stage]);
+        stage += 2;
+        if (stage >= S) { stage -= S; phase ^= 1; }
+        buf += 2;
+        if (buf >= BUFS) { buf -= BUFS; buf_phase ^= 1; }
+    }
+    return true;
+}
+
 template <int BN>
 struct FewCfg {
     static constexpr int kWBytes = BF * BK, kXBytes = BN * BK;
@@ -137,12 +172,12 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
     using C = FewCfg<BN>;
     constexpr int S = C::kStages;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S], acc_full[kBufs], acc_empty[kBufs], sc_full[kBufs],
-        mma_done;
+    __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S], acc_full[kBufs], acc_empty[kBufs], sc_full[2],
+        sc_empty[2], mma_done;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ Groups G;
-    __shared__ __align__(16) float scale[kBufs][BN];
+    __shared__ __align__(16) float scale[2][kScales][BN];
     griddep_launch();
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -155,9 +190,12 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
         for (int i = 0; i < kBufs; ++i) {
             ptx::mbar_init(&acc_full[i], 1);
             ptx::mbar_init(&acc_empty[i], 4);
-            ptx::mbar_init(&sc_full[i], 32);
         }
-        ptx::mbar_init(&mma_done, 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&sc_full[i], 32);
+            ptx::mbar_init(&sc_empty[i], 4);
+        }
+        ptx::mbar_init(&mma_done, 2);
         abort_flag = 0;
         ptx::fence_mbar_init();
         ptx::tma_prefetch_desc(&tma_w);
@@ -198,72 +236,66 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
             if (--stage < 0) { stage = S - 1; phase ^= 1; }
             ptx::mbar_wait(&full_bar[stage], phase, p.status);
         }
-    } else if (warp == 1 && lane == 0) {
-        // ---------------- UMMA
+    } else if ((warp == 1 || warp == kFewIssuer2) && lane == 0) {
+        // ---------------- UMMA, two issuers (see issue_blocks)
         constexpr uint32_t idesc = idesc_e4m3(BF, BN);
-        int stage = 0, buf = 0;
-        uint32_t phase = 0, buf_phase = 0;
-        bool ok = true;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-            for (int kb = 0; kb < p.kb; ++kb) {
-                if (!ptx::mbar_wait(&acc_empty[buf], buf_phase ^ 1, p.status) ||
-                    !ptx::mbar_wait(&full_bar[stage], phase, p.status)) {
-                    abort_flag = 1;
-                    ok = false;
-                    break;
-                }
-                ptx::tc_fence_after();
-                const uint32_t w_addr = ptx::smem_u32(smem + stage * C::kStageBytes);
-                const uint32_t x_addr = w_addr + C::kWBytes;
-                // past K both operands are zero-filled, so a partial last block needs no other form
+        const bool ok = issue_blocks<S, kBufs>(warp == 1 ? 0 : 1, (long long)my_tiles(tiles) * p.kb, full_bar, empty_bar,
+                                              acc_full, acc_empty, p.status, [&](int stage, int buf) {
+            const uint32_t w_addr = ptx::smem_u32(smem + stage * C::kStageBytes);
+            const uint64_t wd = ptx::sdesc_sw128(w_addr, 16, 1024);
+            const uint64_t xd = ptx::sdesc_sw128(w_addr + C::kWBytes, 16, 1024);
 #pragma unroll
-                for (int kk = 0; kk < BK / 32; ++kk)
-                    umma_e4m3(tmem + buf * BN, ptx::sdesc_sw128(w_addr + kk * 32, 16, 1024),
-                              ptx::sdesc_sw128(x_addr + kk * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u);
-                ptx::umma_commit(&empty_bar[stage]);
-                ptx::umma_commit(&acc_full[buf]);
-                if (++stage == S) { stage = 0; phase ^= 1; }
-                if (++buf == kBufs) { buf = 0; buf_phase ^= 1; }
-            }
-        }
+            for (int kk = 0; kk < BK / 32; ++kk)   // K = 32 further: 32 bytes, 2 in the descriptor's units
+                umma_e4m3(tmem + buf * BN, wd + 2 * kk, xd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+        });
+        if (!ok) abort_flag = 1;
         ptx::umma_commit(&mma_done);   // all UMMAs complete before TMEM is released
         ptx::mbar_wait(&mma_done, 0, p.status);
     } else if (warp == 2) {
-        // ---------------- scales
+        // ---------------- scales: the products x_scales * w_scales of kScales blocks at a time, the
+        // next batch's loads under way while the drain works on this one. (One block at a time,
+        // the latency of its loads was the bound: 1100 clocks a block.)
         constexpr int kPer = (BN + 31) / 32;
-        int buf = 0;
-        uint32_t buf_phase = 0;
+        int slot = 0;
+        uint32_t phase = 0;
         bool ok = true;
         for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
             const Tile tl = tile_at(G, p.groups, t, BN, BF);
             const float* ws = p.ws + ((size_t)tl.g * p.nb + tl.f0 / BF) * p.kb;
-            float v[kPer], w;
-            auto load = [&](int kb) {
-                w = ws[kb];
+            float v[kScales][kPer], w[kScales];
+            auto load = [&](int k0) {
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int c = lane + 32 * i;
-                    v[i] = c < tl.rows_left && c < BN ? p.xs[(size_t)kb * p.rows + tl.row0 + c] : 0.f;
+                for (int j = 0; j < kScales; ++j) {
+                    const int kb = min(k0 + j, p.kb - 1);
+                    w[j] = ws[kb];
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) {   // rows behind the last: any scale, their sums are not stored
+                        const int c = min(lane + 32 * i, tl.rows_left - 1);
+                        v[j][i] = p.xs[(size_t)kb * p.rows + tl.row0 + c];
+                    }
                 }
             };
             load(0);
-            for (int kb = 0; kb < p.kb; ++kb) {
-                if (!ptx::mbar_wait(&acc_empty[buf], buf_phase ^ 1, p.status)) { abort_flag = 1; ok = false; break; }
+            for (int k0 = 0; k0 < p.kb; k0 += kScales) {
+                if (!ptx::mbar_wait(&sc_empty[slot], phase ^ 1, p.status)) { abort_flag = 1; ok = false; break; }
 #pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (lane + 32 * i < BN) scale[buf][lane + 32 * i] = v[i] * w;   // one fp32 rounding
-                ptx::mbar_arrive(&sc_full[buf]);
-                if (kb + 1 < p.kb) load(kb + 1);
-                if (++buf == kBufs) { buf = 0; buf_phase ^= 1; }
+                for (int j = 0; j < kScales; ++j)
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i)
+                        if (lane + 32 * i < BN) scale[slot][j][lane + 32 * i] = v[j][i] * w[j];   // one fp32 rounding
+                ptx::mbar_arrive(&sc_full[slot]);
+                if (k0 + kScales < p.kb) load(k0 + kScales);
+                slot ^= 1;
+                if (slot == 0) phase ^= 1;
             }
         }
-    } else if (warp >= 3) {
+    } else if (warp >= 3 && warp < 7) {
         // ---------------- drain: thread = feature of TMEM lane quarter warp & 3
         const int quarter = warp & 3;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         float* ebuf = reinterpret_cast<float*>(smem + S * C::kStageBytes + (warp - 3) * C::kEpiBuf);
-        int buf = 0;
-        uint32_t buf_phase = 0;
+        int buf = 0, slot = 0;
+        uint32_t buf_phase = 0, sc_phase = 0;
         bool ok = true;
         for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
             const Tile tl = tile_at(G, p.groups, t, BN, BF);
@@ -271,31 +303,48 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
 #pragma unroll
             for (int c = 0; c < BN; ++c) acc[c] = 0.f;
             for (int kb = 0; kb < p.kb; ++kb) {
-                if (!ptx::mbar_wait(&acc_full[buf], buf_phase, p.status) ||
-                    !ptx::mbar_wait(&sc_full[buf], buf_phase, p.status)) {
+                const int j = kb % kScales;
+                if ((j == 0 && !ptx::mbar_wait(&sc_full[slot], sc_phase, p.status)) ||
+                    !ptx::mbar_wait(&acc_full[buf], buf_phase, p.status)) {
                     abort_flag = 1;
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
+                // kGroup columns in flight; the accumulator is free once the last are in registers
+                constexpr int kGroup = BN < 64 ? BN : 64;
 #pragma unroll
-                for (int c0 = 0; c0 < BN; c0 += 16) {
-                    uint32_t d[16];
-                    ptx::tmem_ld16_nowait(t_lane + buf * BN + c0, d);
-                    ptx::tmem_wait_ld16(d);
-                    const float4* s4 = reinterpret_cast<const float4*>(&scale[buf][c0]);
+                for (int g0 = 0; g0 < BN; g0 += kGroup) {
+                    uint32_t d[kGroup / 16][16];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 s = s4[j];
-                        acc[c0 + 4 * j] = fmaf(__uint_as_float(d[4 * j]), s.x, acc[c0 + 4 * j]);
-                        acc[c0 + 4 * j + 1] = fmaf(__uint_as_float(d[4 * j + 1]), s.y, acc[c0 + 4 * j + 1]);
-                        acc[c0 + 4 * j + 2] = fmaf(__uint_as_float(d[4 * j + 2]), s.z, acc[c0 + 4 * j + 2]);
-                        acc[c0 + 4 * j + 3] = fmaf(__uint_as_float(d[4 * j + 3]), s.w, acc[c0 + 4 * j + 3]);
+                    for (int c = 0; c < kGroup / 16; ++c) ptx::tmem_ld16_nowait(t_lane + buf * BN + g0 + 16 * c, d[c]);
+#pragma unroll
+                    for (int c = 0; c < kGroup / 16; ++c) ptx::tmem_wait_ld16(d[c]);
+                    if (g0 + kGroup == BN) {
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(&acc_empty[buf]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < kGroup / 16; ++c) {
+                        const float4* s4 = reinterpret_cast<const float4*>(&scale[slot][j][g0 + 16 * c]);
+                        float* a16 = acc + g0 + 16 * c;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 s = s4[i];
+                            a16[4 * i] = fmaf(__uint_as_float(d[c][4 * i]), s.x, a16[4 * i]);
+                            a16[4 * i + 1] = fmaf(__uint_as_float(d[c][4 * i + 1]), s.y, a16[4 * i + 1]);
+                            a16[4 * i + 2] = fmaf(__uint_as_float(d[c][4 * i + 2]), s.z, a16[4 * i + 2]);
+                            a16[4 * i + 3] = fmaf(__uint_as_float(d[c][4 * i + 3]), s.w, a16[4 * i + 3]);
+                        }
                     }
                 }
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&acc_empty[buf]);
+                if (j == kScales - 1 || kb == p.kb - 1) {   // the batch is read
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&sc_empty[slot]);
+                    slot ^= 1;
+                    if (slot == 0) sc_phase ^= 1;
+                }
                 if (++buf == kBufs) { buf = 0; buf_phase ^= 1; }
             }
             if (!ok) break;
@@ -347,111 +396,160 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
 }
 
 // ------------------------------------------------------------------ many rows per group
-// k_fp8_many: M = 128 rows x N = bn features (a multiple of 32, 64 .. 256, chosen by the host to
-// fill the last wave), the rows as the UMMA's A operand. TMEM lane = row, so an epilogue thread
-// needs one scale product per block (two where its columns straddle a 128-feature boundary)
-// instead of one per column, and 256-wide tiles let each operand byte in shared memory feed
-// enough tensor work. Eight drain warps: two per lane quarter, each with half of the columns and
-// its fp32 sums in registers (setmaxnreg moves the other warps' registers to them); two TMEM
-// accumulators of 256 columns.
+// k_fp8_many: a pair of CTAs on a tile of 256 rows x 256 features, the rows as the UMMA's A
+// operand (cta_group::2, M = 256: each CTA holds 128 rows of x, the weight rows are split
+// between the two, and each CTA's tensor core reads both halves). TMEM lane = row, so a drain
+// thread needs one scale per block and not one per column.
+//
+// Why a pair: a block of a 128 x 256 tile of one CTA takes 48 KB of operands for 512 tensor
+// clocks, and an SM takes in about 64 bytes a clock from L2 (390 ns a block measured with the
+// drain left out: 62 bytes a clock); the pair needs 32 KB a CTA. Why sixteen drain warps: the
+// drain of a block is a chain of waits (for the accumulator, for TMEM loads) and 256 issue
+// slots of additions on each scheduler; four warps of 64 columns each on a scheduler hide one
+// another's waits, which two of 128 columns did not (1235 clocks a block).
+//
+// Warps 0-3 (32 registers): 0 TMA, 1 and 2 UMMA (leader only; every second block each, see
+// issue_blocks), 3 scales and TMEM. Warps 4-19 (112 registers): the drain, four warps to 64
+// columns, the fp32 sums in each thread's registers.
 constexpr int kManyThreads = 384;
-constexpr int kManyRows = 128;
-constexpr int kManyMaxBn = 256;
+constexpr int kManyRows = 128;                        // rows of a CTA; the pair has twice as many
+constexpr int kManyFeatures = 256;
 constexpr int kManyABytes = kManyRows * BK;
-constexpr int kManyStageBytes = kManyABytes + kManyMaxBn * BK;
-constexpr int kManyStages = 4;
-constexpr int kManyEpiBuf = 32 * 64;    // per drain warp: 32 rows x 64 bytes
-constexpr int kManySmem = kManyStages * kManyStageBytes + 8 * kManyEpiBuf + 1024;
+constexpr int kManyWBytes = kManyFeatures / 2 * BK;   // this CTA's weight rows
+constexpr int kManyStageBytes = kManyABytes + kManyWBytes;
+constexpr int kManyStages = 6;
+constexpr int kManyDrain = 8;                         // drain warps
+constexpr int kManyEpiBuf = 32 * 64;                  // per drain warp: 32 rows x 64 bytes
+constexpr int kManySmem = kManyStages * kManyStageBytes + kManyDrain * kManyEpiBuf + 1024;
 
-__device__ __forceinline__ void fma_f32x2(uint64_t& acc, uint32_t d0, uint32_t d1, uint64_t s) {
-    asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}" : "+l"(acc) : "r"(d0), "r"(d1), "l"(s));
+// 4-byte asynchronous copy, counted by cp.async.mbarrier.arrive.
+__device__ __forceinline__ void cp_async_4(float* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
+// One CTA's load of a pair's stage: into its own shared memory, counted on the leader's barrier.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m, uint32_t bar_cluster, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4}], [%2];" ::"r"(ptx::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(x), "r"(y)
+        : "memory");
 }
-__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
+__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on a barrier of the pair (a shared::cluster address). What it orders are TMEM reads, which the
+// tcgen05 fences on both sides cover, so the arrive itself is relaxed: a release (which
+// publishes memory writes too) held the warp up, about 250 clocks at CTA and 1300 at cluster scope.
+__device__ __forceinline__ void arrive_cluster(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+// Arrive on the barrier at this offset in both CTAs once this thread's earlier UMMAs have completed.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            ptx::smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
 }
 
-__global__ void __launch_bounds__(kManyThreads, 1)
-k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w, Problem p, int bn) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kManyThreads, 1)
+k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w, Problem p) {
     constexpr int S = kManyStages;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S], acc_full[2], acc_empty[2], mma_done;
+    __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S], acc_full[2], acc_empty[2], sc_full[2], sc_empty[2],
+        mma_done;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ Groups G;
+    __shared__ float x_sc[2][kScales][kManyRows];
+    __shared__ float w_sc[2][kScales][2];
     griddep_launch();
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)ptx::cluster_ctarank(), pair = (int)ptx::cluster_id_x(), pairs = (int)ptx::nclusters_x();
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            ptx::mbar_init(&full_bar[i], 1);
-            ptx::mbar_init(&empty_bar[i], 1);
+            ptx::mbar_init(&full_bar[i], 1);     // the leader's: its producer, and both CTAs' bytes
+            ptx::mbar_init(&empty_bar[i], 1);    // the leader's commit
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&acc_full[i], 1);
-            ptx::mbar_init(&acc_empty[i], 8);
+            ptx::mbar_init(&acc_empty[i], 2 * kManyDrain);   // the leader's: the drain warps of both CTAs
+            ptx::mbar_init(&sc_full[i], 32);
+            ptx::mbar_init(&sc_empty[i], kManyDrain);
         }
-        ptx::mbar_init(&mma_done, 1);
+        ptx::mbar_init(&mma_done, 2);
         abort_flag = 0;
         ptx::fence_mbar_init();
         ptx::tma_prefetch_desc(&tma_x);
         ptx::tma_prefetch_desc(&tma_w);
     }
-    if (warp == 2) {
-        ptx::tmem_alloc(&tmem_slot, 512);
-        ptx::tmem_relinquish();
+    if (warp == 3) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_u32(&tmem_slot)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     griddep_wait();
-    build_groups(G, p, kManyRows, (p.n + bn - 1) / bn);
+    build_groups(G, p, 2 * kManyRows, (p.n + kManyFeatures - 1) / kManyFeatures);
     ptx::tc_fence_before();
     __syncthreads();
+    ptx::cluster_sync_all();   // the peer's barriers are set up before anything arrives on them
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const int tiles = G.start[p.groups];
+    // Features of a tile, a multiple of 16: the UMMA's N. The first half are the leader's weight rows.
+    auto width_of = [&](int f0) { return min(kManyFeatures, p.n - f0); };
 
     if (warp < 4) {
         // 128 x 72 + 256 x 216 registers = 384 x 168, what the block was launched with
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0 && lane == 0) {
-            // ---------------- TMA
-            const uint32_t bytes = kManyABytes + bn * BK;
+            // ---------------- TMA: this CTA's rows of x and of the weight tile
             int stage = 0, issued = 0;
             uint32_t phase = 0;
-            for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-                const Tile tl = tile_at(G, p.groups, t, kManyRows, bn);
+            for (int t = pair; t < tiles; t += pairs) {
+                const Tile tl = tile_at(G, p.groups, t, 2 * kManyRows, kManyFeatures);
+                const int x_row = tl.row0 + rank * kManyRows;
+                const int w_row = tl.g * p.n + tl.f0 + rank * (width_of(tl.f0) / 2);
                 for (int kb = 0; kb < p.kb; ++kb) {
                     if (!ptx::mbar_wait(&empty_bar[stage], phase ^ 1, p.status)) { abort_flag = 1; goto loads_done; }
                     if (*(volatile int*)&abort_flag) goto loads_done;
                     unsigned char* x_s = smem + stage * kManyStageBytes;
-                    ptx::mbar_arrive_expect_tx(&full_bar[stage], bytes);
-                    ptx::tma_load_2d(x_s, &tma_x, &full_bar[stage], kb * BK, tl.row0);
-                    ptx::tma_load_2d(x_s + kManyABytes, &tma_w, &full_bar[stage], kb * BK, tl.g * p.n + tl.f0);
+                    const uint32_t bar = ptx::mapa_shared(ptx::smem_u32(&full_bar[stage]), 0);
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(&full_bar[stage], 2 * kManyStageBytes);
+                    tma_load_2d_pair(x_s, &tma_x, bar, kb * BK, x_row);
+                    tma_load_2d_pair(x_s + kManyABytes, &tma_w, bar, kb * BK, w_row);
                     ++issued;
                     if (++stage == S) { stage = 0; phase ^= 1; }
                 }
             }
         loads_done:
-            for (int i = 0; i < S && i < issued; ++i) {   // every load lands before shared memory is released
-                if (--stage < 0) { stage = S - 1; phase ^= 1; }
-                ptx::mbar_wait(&full_bar[stage], phase, p.status);
-            }
-        } else if (warp == 1 && lane == 0) {
-            // ---------------- UMMA
-            const uint32_t idesc = idesc_e4m3(kManyRows, bn);
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, buf_phase = 0;
+            if (rank == 0)   // both CTAs' loads land before shared memory is released (the pair leaves together)
+                for (int i = 0; i < S && i < issued; ++i) {
+                    if (--stage < 0) { stage = S - 1; phase ^= 1; }
+                    ptx::mbar_wait(&full_bar[stage], phase, p.status);
+                }
+        } else if ((warp == 1 || warp == 2) && lane == 0 && rank == 0) {
+            // ---------------- UMMA: every second K block each
+            const int q = warp - 1;
+            int stage = q;
+            uint32_t phase = 0, acc_phase = 0;
+            long long next = q, before = 0;   // blocks, over all tiles of the pair
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-                for (int kb = 0; kb < p.kb; ++kb) {
-                    if (!ptx::mbar_wait(&acc_empty[buf], buf_phase ^ 1, p.status) ||
-                        !ptx::mbar_wait(&full_bar[stage], phase, p.status)) {
+            for (int t = pair; ok && t < tiles; t += pairs) {
+                const uint32_t idesc =
+                    idesc_e4m3(2 * kManyRows, width_of(tile_at(G, p.groups, t, 2 * kManyRows, kManyFeatures).f0));
+                for (; next < before + p.kb; next += 2) {
+                    if (!ptx::mbar_wait(&full_bar[stage], phase, p.status) ||
+                        !ptx::mbar_wait(&acc_empty[q], acc_phase ^ 1, p.status)) {
                         abort_flag = 1;
                         ok = false;
                         break;
@@ -460,99 +558,138 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
                     const uint32_t x_addr = ptx::smem_u32(smem + stage * kManyStageBytes);
                     const uint64_t xd = ptx::sdesc_sw128(x_addr, 16, 1024);
                     const uint64_t wd = ptx::sdesc_sw128(x_addr + kManyABytes, 16, 1024);
+                    // past K both operands are zero-filled, so a partial last block has no other form
 #pragma unroll
                     for (int kk = 0; kk < BK / 32; ++kk)   // K = 32 further: 32 bytes, 2 in the descriptor's units
-                        umma_e4m3(tmem + buf * 256, xd + 2 * kk, wd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
-                    ptx::umma_commit(&empty_bar[stage]);
-                    ptx::umma_commit(&acc_full[buf]);
-                    if (++stage == S) { stage = 0; phase ^= 1; }
-                    buf ^= 1;
-                    if (buf == 0) buf_phase ^= 1;
+                        umma_e4m3_pair(tmem + q * kManyFeatures, xd + 2 * kk, wd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+                    umma_commit_pair(&acc_full[q]);
+                    umma_commit_pair(&empty_bar[stage]);
+                    acc_phase ^= 1;
+                    stage += 2;
+                    if (stage >= S) { stage -= S; phase ^= 1; }
+                }
+                before += p.kb;
+            }
+            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                             ptx::smem_u32(&mma_done))
+                         : "memory");   // all UMMAs complete before TMEM is released
+            ptx::mbar_wait(&mma_done, 0, p.status);
+        } else if (warp == 3) {
+            // ---------------- scales: 128 row scales and two weight scales a block, kScales blocks
+            // at a time and one such batch ahead (a load's latency is longer than a block's product,
+            // and each hand-over costs the drain a wait)
+            int slot = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = pair; ok && t < tiles; t += pairs) {
+                const Tile tl = tile_at(G, p.groups, t, 2 * kManyRows, kManyFeatures);
+                const int r0 = tl.row0 + rank * kManyRows + lane;
+                const float* ws = p.ws + ((size_t)tl.g * p.nb + min((tl.f0 >> 7) + (lane & 1), p.nb - 1)) * p.kb + (lane >> 1);
+                for (int k0 = 0; k0 < p.kb; k0 += kScales) {
+                    if (!ptx::mbar_wait(&sc_empty[slot], phase ^ 1, p.status)) { abort_flag = 1; ok = false; break; }
+                    const int nk = min(kScales, p.kb - k0);
+                    for (int j = 0; j < nk; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)   // rows behind the last: any scale, their sums are not stored
+                            cp_async_4(&x_sc[slot][j][lane + 32 * i],
+                                       p.xs + (size_t)(k0 + j) * p.rows + min(r0 + 32 * i, p.rows - 1));
+                    if (lane < 2 * nk) cp_async_4(&w_sc[slot][lane >> 1][lane & 1], ws + k0);
+                    ptx::cp_async_arrive_noinc(&sc_full[slot]);
+                    slot ^= 1;
+                    if (slot == 0) phase ^= 1;
                 }
             }
-            ptx::umma_commit(&mma_done);
-            ptx::mbar_wait(&mma_done, 0, p.status);
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        // ---------------- drain: thread = row of TMEM lane quarter warp & 3, columns [c0, c0 + bn / 2)
-        const int quarter = warp & 3, half = bn >> 1, c0 = ((warp - 4) >> 2) * half, chunks = half >> 4;
-        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
-        unsigned char* ebuf = smem + S * kManyStageBytes + (warp - 4) * kManyEpiBuf;
-        int buf = 0;
-        uint32_t buf_phase = 0;
+        // ---------------- drain: thread = row of TMEM lane quarter warp & 3, columns [128 cg, 128 cg + 128)
+        const int quarter = warp & 3, cg = (warp - 4) >> 2;
+        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + 128 * cg;
+        const uint32_t freed = ptx::mapa_shared(ptx::smem_u32(&acc_empty[0]), 0);   // the leader's
+        const float* my_x = &x_sc[0][0][quarter * 32 + lane];
+        const float* my_w = &w_sc[0][0][cg];
+        int slot = 0, q = 0;
+        uint32_t sc_phase = 0, acc_phase = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-            const Tile tl = tile_at(G, p.groups, t, kManyRows, bn);
-            // columns of chunk c belong to scale block b0 while c < cut, to b0 + 1 from there on
-            const int f = tl.f0 + c0, b0 = f >> 7, cut = (128 - (f & 127)) >> 4;
-            const float* ws0 = p.ws + ((size_t)tl.g * p.nb + min(b0, p.nb - 1)) * p.kb;
-            const float* ws1 = p.ws + ((size_t)tl.g * p.nb + min(b0 + 1, p.nb - 1)) * p.kb;
-            const int r = quarter * 32 + lane;
-            const float* xs = p.xs + tl.row0 + min(r, tl.rows_left - 1);
-            uint64_t acc[8][8];
+        for (int t = pair; ok && t < tiles; t += pairs) {
+            float acc[4][32];
+            uint32_t d[2][32];
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) acc[c][i] = 0;
-            // scales of the next two blocks, loaded two blocks ahead
-            float nx[2], n0[2], n1[2];
-            auto fetch = [&](int kb) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int b = min(kb + j, p.kb - 1);
-                    nx[j] = xs[(size_t)b * p.rows];
-                    n0[j] = ws0[b];
-                    n1[j] = ws1[b];
-                }
-            };
-            fetch(0);
-            for (int kb2 = 0; ok && kb2 < p.kb; kb2 += 2) {
-                const float sa[2] = {nx[0] * n0[0], nx[1] * n0[1]}, sb[2] = {nx[0] * n1[0], nx[1] * n1[1]};
-                fetch(kb2 + 2);
-#pragma unroll 1
-                for (int j = 0; j < 2 && kb2 + j < p.kb; ++j) {
-                    const uint64_t lo = j == 0 ? pack_f32x2(sa[0], sa[0]) : pack_f32x2(sa[1], sa[1]);
-                    const uint64_t hi = j == 0 ? pack_f32x2(sb[0], sb[0]) : pack_f32x2(sb[1], sb[1]);
-                    if (!ptx::mbar_wait(&acc_full[buf], buf_phase, p.status)) {
-                        abort_flag = 1;
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after();
-                    uint32_t d[2][16];
-                    ptx::tmem_ld16_nowait(t_lane + buf * 256, d[0]);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        if (c >= chunks) break;
-                        ptx::tmem_wait_ld16(d[c & 1]);
-                        if (c + 1 < chunks && c + 1 < 8)
-                            ptx::tmem_ld16_nowait(t_lane + buf * 256 + 16 * (c + 1), d[(c + 1) & 1]);
-                        const uint64_t s = c < cut ? lo : hi;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) fma_f32x2(acc[c][i], d[c & 1][2 * i], d[c & 1][2 * i + 1], s);
-                    }
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&acc_empty[buf]);
-                    buf ^= 1;
-                    if (buf == 0) buf_phase ^= 1;
-                }
+            for (int i = 0; i < 32; ++i) {
+                acc[0][i] = acc[1][i] = acc[2][i] = acc[3][i] = 0.f;
+                d[1][i] = 0;
             }
-            if (!ok) break;
+            auto add = [&](float (&sum)[32], const uint32_t (&v)[32], float by) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) sum[i] = fmaf(__uint_as_float(v[i]), by, sum[i]);
+            };
+            // A block's scale (one fp32 rounding) is fetched while the block before it is drained;
+            // 32 columns load while 32 are added, the last 32 of a block while the next one's
+            // first load.
+            float s = 0.f, s_next = 0.f;
+            if (ptx::mbar_wait(&sc_full[slot], sc_phase, p.status))
+                s_next = my_x[slot * kScales * kManyRows] * my_w[slot * kScales * 2];
+            else
+                ok = false;
+            for (int kb = 0; ok && kb < p.kb; ++kb) {
+                const float s_prev = s;
+                s = s_next;
+                if (!ptx::mbar_wait(&acc_full[q], acc_phase, p.status)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t src = t_lane + q * kManyFeatures;
+                ptx::tmem_ld32_nowait(src, d[0]);
+                const int j = (kb + 1) % kScales;
+                if (j == 0 || kb + 1 == p.kb) {   // the batch is read
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&sc_empty[slot]);
+                    slot ^= 1;
+                    if (slot == 0) sc_phase ^= 1;
+                    if (kb + 1 < p.kb && !ptx::mbar_wait(&sc_full[slot], sc_phase, p.status)) ok = false;
+                }
+                if (kb + 1 < p.kb)
+                    s_next = my_x[(slot * kScales + j) * kManyRows] * my_w[(slot * kScales + j) * 2];
+                add(acc[3], d[1], s_prev);
+                ptx::tmem_wait_ld32(d[0]);
+                ptx::tmem_ld32_nowait(src + 32, d[1]);
+                add(acc[0], d[0], s);
+                ptx::tmem_wait_ld32(d[1]);
+                ptx::tmem_ld32_nowait(src + 64, d[0]);
+                add(acc[1], d[1], s);
+                ptx::tmem_wait_ld32(d[0]);
+                ptx::tmem_ld32_nowait(src + 96, d[1]);
+                add(acc[2], d[0], s);
+                ptx::tmem_wait_ld32(d[1]);
+                ptx::tc_fence_before();   // all in registers: the accumulator is free
+                __syncwarp();
+                if (lane == 0) arrive_cluster(freed + 8 * q);
+                q ^= 1;
+                if (q == 0) acc_phase ^= 1;
+            }
+            if (!ok) {
+                abort_flag = 1;
+                break;
+            }
+            add(acc[3], d[1], s);
+            const Tile tl = tile_at(G, p.groups, t, 2 * kManyRows, kManyFeatures);
+            unsigned char* ebuf = smem + S * kManyStageBytes + (warp - 4) * kManyEpiBuf;
+            const int f = tl.f0 + 128 * cg, row0 = rank * kManyRows + quarter * 32;
             // Out through shared memory, 64 bytes a row at a time (32 16-bit or 16 fp32 columns):
             // 16-byte pieces, swizzled by the row so that neither side has bank conflicts; four
             // lanes store one row's piece of a line.
-            const int rows = min(32, tl.rows_left - quarter * 32);   // this warp's rows (<= 0: none)
-            auto store_rows = [&](int col, int cols, int esize) {
+            const int rows = min(32, tl.rows_left - row0);   // this warp's rows (<= 0: none)
+            auto store_rows = [&](int col, int esize) {
                 __syncwarp();
                 const int piece = lane & 3, pc = col + piece * 16 / esize;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int rr = 8 * i + (lane >> 2);
-                    if (rr < rows && pc < col + cols && f + pc < p.n)
+                    if (rr < rows && f + pc < p.n)
                         *reinterpret_cast<uint4*>(static_cast<unsigned char*>(p.out) +
-                                                  ((size_t)(tl.row0 + quarter * 32 + rr) * p.n + f + pc) * esize) =
+                                                  ((size_t)(tl.row0 + row0 + rr) * p.n + f + pc) * esize) =
                             *reinterpret_cast<const uint4*>(ebuf + rr * 64 + ((piece ^ ((rr >> 1) & 3)) << 4));
                 }
                 __syncwarp();
@@ -563,46 +700,44 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
             if (p.dtype == kDtypeFp32) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    if (c >= chunks) break;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float2 a = unpack_f32x2(acc[c][2 * q]), b = unpack_f32x2(acc[c][2 * q + 1]);
-                        *piece_at(q) = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
-                                                  __float_as_uint(b.y));
+                    for (int v = 0; v < 4; ++v) {
+                        const float* e = &acc[c >> 1][16 * (c & 1) + 4 * v];
+                        *reinterpret_cast<float4*>(piece_at(v)) = make_float4(e[0], e[1], e[2], e[3]);
                     }
-                    store_rows(16 * c, 16, 4);
+                    store_rows(16 * c, 4);
                 }
             } else {
                 const bool to_bf16 = p.dtype == kDtypeBf16;
 #pragma unroll
-                for (int c = 0; c < 8; c += 2) {
-                    if (c >= chunks) break;
+                for (int c = 0; c < 4; ++c) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int v = 0; v < 4; ++v) {
                         uint32_t o[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float2 a = unpack_f32x2(acc[c + (q >> 1)][4 * (q & 1) + i]);
+                            const float ax = acc[c][8 * v + 2 * i], ay = acc[c][8 * v + 2 * i + 1];
                             if (to_bf16) {
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(a.x, a.y);
-                                o[i] = *reinterpret_cast<const uint32_t*>(&h);
+                                const __nv_bfloat162 p2 = __floats2bfloat162_rn(ax, ay);
+                                o[i] = *reinterpret_cast<const uint32_t*>(&p2);
                             } else {
-                                const __half2 h = __floats2half2_rn(a.x, a.y);
-                                o[i] = *reinterpret_cast<const uint32_t*>(&h);
+                                const __half2 p2 = __floats2half2_rn(ax, ay);
+                                o[i] = *reinterpret_cast<const uint32_t*>(&p2);
                             }
                         }
-                        *piece_at(q) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *piece_at(v) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
-                    store_rows(16 * c, min(32, half - 16 * c), 2);
+                    store_rows(32 * c, 2);
                 }
             }
         }
     }
     ptx::tc_fence_before();
     __syncthreads();
-    if (warp == 2) {
+    ptx::cluster_sync_all();   // no UMMA reads the peer's memory, no arrival is under way any more
+    if (warp == 3) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, 512);
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
 }
 

@@ -40,9 +40,27 @@ cudaError_t launch_few(const void* x, const void* w, const fp8::Problem& p, cuda
     if (!make_tma_2d(&tw, w, (uint64_t)p.k, (uint64_t)p.groups * p.n, (uint64_t)p.k, fp8::BK, fp8::BF, 128, 1) ||
         !make_tma_2d(&tx, x, (uint64_t)p.k, (uint64_t)p.rows, (uint64_t)p.k, fp8::BK, BN, 128, 1))
         return cudaErrorInvalidValue;
-    const long long tiles = ((long long)(p.rows + BN - 1) / BN + p.groups - 1) * ((p.n + fp8::BF - 1) / fp8::BF);
-    const int grid = (int)std::min<long long>(tiles, sms_of(dev));
-    return launch_pdl(kern, dim3(grid), dim3(fp8::kFewThreads), C::kSmem, s, tw, tx, p);
+    // Tiles there can be: a row tile for every BN rows and one more for each group that has rows.
+    const int sms = sms_of(dev), f_tiles = (p.n + fp8::BF - 1) / fp8::BF;
+    const long long tiles = ((long long)(p.rows - 1) / BN + std::min(p.groups, p.rows)) * f_tiles;
+    // Few tiles leave SMs idle and a long chain of K blocks to each: split K as far as the SMs
+    // and at least two blocks a CTA go.
+    fp8::Problem q = p;
+    while (q.split < 8 && tiles * q.split * 2 <= sms && p.kb >= 4 * q.split) q.split *= 2;
+    const int grid = (int)std::min<long long>(tiles, sms) * q.split;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(fp8::kFewThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    if (q.split == 1) return launch_pdl(kern, dim3(grid), dim3(fp8::kFewThreads), C::kSmem, s, tw, tx, q);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = q.split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, tw, tx, q);
 }
 
 cudaError_t launch_many(const void* x, const void* w, const fp8::Problem& p, cudaStream_t s) {
@@ -73,7 +91,7 @@ bool fp8_gemm_fits(int rows, int groups, int n) {
 cudaError_t launch_fp8_gemm(const void* x, const float* xs, const void* w, const float* ws, const int32_t* offsets,
                             int rows, int groups, int n, int k, void* out, int dtype, int32_t* status,
                             cudaStream_t s) {
-    fp8::Problem p{xs, ws, offsets, rows, groups, n, k, (n + 127) / 128, (k + 127) / 128, out, dtype, status};
+    fp8::Problem p{xs, ws, offsets, rows, groups, n, k, (n + 127) / 128, (k + 127) / 128, out, dtype, status, 1};
     const long long per_group = ((long long)rows + groups - 1) / groups;
     if (per_group <= 16) return launch_few<16>(x, w, p, s);
     if (per_group <= 32) return launch_few<32>(x, w, p, s);

@@ -16,8 +16,10 @@
 // k_fp8_few: few rows per group, where the weights' bytes bound the product: the weight tile
 // is the UMMA's A operand (M = 128 features), the rows its B operand (N = BN rows), so a
 // group of few rows costs few tensor cycles, and TMEM lane = feature, column = row.
-// Warp 0 issues TMA, warp 1 UMMA, warp 2 brings the scales x_scales * w_scales of each block
-// into shared memory (every epilogue thread needs all of them), warps 3-6 drain.
+// Warp 0 issues TMA, warps 1 and 7 UMMA, warp 2 brings the scales x_scales * w_scales of each
+// block into shared memory (every drain thread needs all of them), warps 3-6 drain. Where the
+// tiles are few, a cluster of `split` CTAs takes one tile, each a run of its K blocks; the
+// partial sums meet in distributed shared memory and are added in the order of the ranks.
 #pragma once
 
 #include <cuda.h>
@@ -45,6 +47,7 @@ struct Problem {
     void* out;
     int dtype;
     int32_t* status;
+    int split;                   // k_fp8_few: CTAs (a cluster) that share a tile's K blocks
 };
 
 // Instruction descriptor, kind::f8f6f4: e4m3 A and B (both K-major), fp32 D.
@@ -123,9 +126,14 @@ __device__ __forceinline__ Tile tile_at(const Groups& G, int groups, int t, int 
     return Tile{lo, G.bound[lo] + rt * rows_per_tile, rows - rt * rows_per_tile, ft * bf};
 }
 
-// Tiles of this CTA.
-__device__ __forceinline__ int my_tiles(int tiles) {
-    return (int)blockIdx.x < tiles ? (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+// Tiles t0, t0 + step, ... below `tiles`.
+__device__ __forceinline__ int my_tiles(int tiles, int t0, int step) {
+    return t0 < tiles ? (tiles - 1 - t0) / step + 1 : 0;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // The UMMAs of every second K block of the CTA, from block `first` on; total: all its tiles'
@@ -212,14 +220,17 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const int tiles = G.start[p.groups];
+    const int rank = p.split > 1 ? (int)ptx::cluster_ctarank() : 0;
+    const int t0 = blockIdx.x / p.split, t_step = gridDim.x / p.split;   // with a split: one tile at most
+    const int kb0 = (int)((long long)p.kb * rank / p.split), kb1 = (int)((long long)p.kb * (rank + 1) / p.split);
 
     if (warp == 0 && lane == 0) {
         // ---------------- TMA
         int stage = 0, issued = 0;
         uint32_t phase = 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        for (int t = t0; t < tiles; t += t_step) {
             const Tile tl = tile_at(G, p.groups, t, BN, BF);
-            for (int kb = 0; kb < p.kb; ++kb) {
+            for (int kb = kb0; kb < kb1; ++kb) {
                 if (!ptx::mbar_wait(&empty_bar[stage], phase ^ 1, p.status)) { abort_flag = 1; goto loads_done; }
                 if (*(volatile int*)&abort_flag) goto loads_done;
                 unsigned char* w_s = smem + stage * C::kStageBytes;
@@ -239,7 +250,7 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
     } else if ((warp == 1 || warp == kFewIssuer2) && lane == 0) {
         // ---------------- UMMA, two issuers (see issue_blocks)
         constexpr uint32_t idesc = idesc_e4m3(BF, BN);
-        const bool ok = issue_blocks<S, kBufs>(warp == 1 ? 0 : 1, (long long)my_tiles(tiles) * p.kb, full_bar, empty_bar,
+        const bool ok = issue_blocks<S, kBufs>(warp == 1 ? 0 : 1, (long long)my_tiles(tiles, t0, t_step) * (kb1 - kb0), full_bar, empty_bar,
                                               acc_full, acc_empty, p.status, [&](int stage, int buf) {
             const uint32_t w_addr = ptx::smem_u32(smem + stage * C::kStageBytes);
             const uint64_t wd = ptx::sdesc_sw128(w_addr, 16, 1024);
@@ -259,14 +270,14 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
         int slot = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+        for (int t = t0; ok && t < tiles; t += t_step) {
             const Tile tl = tile_at(G, p.groups, t, BN, BF);
             const float* ws = p.ws + ((size_t)tl.g * p.nb + tl.f0 / BF) * p.kb;
             float v[kScales][kPer], w[kScales];
             auto load = [&](int k0) {
 #pragma unroll
                 for (int j = 0; j < kScales; ++j) {
-                    const int kb = min(k0 + j, p.kb - 1);
+                    const int kb = min(k0 + j, kb1 - 1);
                     w[j] = ws[kb];
 #pragma unroll
                     for (int i = 0; i < kPer; ++i) {   // rows behind the last: any scale, their sums are not stored
@@ -275,8 +286,8 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
                     }
                 }
             };
-            load(0);
-            for (int k0 = 0; k0 < p.kb; k0 += kScales) {
+            load(kb0);
+            for (int k0 = kb0; k0 < kb1; k0 += kScales) {
                 if (!ptx::mbar_wait(&sc_empty[slot], phase ^ 1, p.status)) { abort_flag = 1; ok = false; break; }
 #pragma unroll
                 for (int j = 0; j < kScales; ++j)
@@ -284,7 +295,7 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
                     for (int i = 0; i < kPer; ++i)
                         if (lane + 32 * i < BN) scale[slot][j][lane + 32 * i] = v[j][i] * w[j];   // one fp32 rounding
                 ptx::mbar_arrive(&sc_full[slot]);
-                if (k0 + kScales < p.kb) load(k0 + kScales);
+                if (k0 + kScales < kb1) load(k0 + kScales);
                 slot ^= 1;
                 if (slot == 0) phase ^= 1;
             }
@@ -297,13 +308,13 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
         int buf = 0, slot = 0;
         uint32_t buf_phase = 0, sc_phase = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+        for (int t = t0; ok && t < tiles; t += t_step) {
             const Tile tl = tile_at(G, p.groups, t, BN, BF);
             float acc[BN];
 #pragma unroll
             for (int c = 0; c < BN; ++c) acc[c] = 0.f;
-            for (int kb = 0; kb < p.kb; ++kb) {
-                const int j = kb % kScales;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const int j = (kb - kb0) % kScales;
                 if ((j == 0 && !ptx::mbar_wait(&sc_full[slot], sc_phase, p.status)) ||
                     !ptx::mbar_wait(&acc_full[buf], buf_phase, p.status)) {
                     abort_flag = 1;
@@ -339,7 +350,7 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
                         }
                     }
                 }
-                if (j == kScales - 1 || kb == p.kb - 1) {   // the batch is read
+                if (j == kScales - 1 || kb == kb1 - 1) {   // the batch is read
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&sc_empty[slot]);
                     slot ^= 1;
@@ -348,6 +359,12 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
                 if (++buf == kBufs) { buf = 0; buf_phase ^= 1; }
             }
             if (!ok) break;
+            if (p.split > 1) {   // partial sums [row][feature] where the stages were: every load and UMMA is over
+                float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+                for (int c = 0; c < BN; ++c) part[c * BF + quarter * 32 + lane] = acc[c];
+                continue;
+            }
             // 16 rows at a time through shared memory: a row's 32 features are stored side by side
             const int f = tl.f0 + quarter * 32;
 #pragma unroll
@@ -389,6 +406,30 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
     }
     ptx::tc_fence_before();
     __syncthreads();
+    if (p.split > 1) {
+        ptx::cluster_sync_all();   // all ranks' partial sums are there
+        if (t0 < tiles) {
+            const Tile tl = tile_at(G, p.groups, t0, BN, BF);
+            const int f = threadIdx.x % BF;
+            const uint32_t mine = ptx::smem_u32(smem);
+            for (int c = rank + p.split * (threadIdx.x / BF); c < min(BN, tl.rows_left); c += p.split * (kFewThreads / BF)) {
+                float v[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    v[r] = r < p.split ? ld_cluster_f32(ptx::mapa_shared(mine, r) + 4 * (c * BF + f)) : 0.f;
+                float sum = v[0];
+#pragma unroll
+                for (int r = 1; r < 8; ++r) sum += v[r];
+                if (tl.f0 + f < p.n) {
+                    const size_t at = (size_t)(tl.row0 + c) * p.n + tl.f0 + f;
+                    if (p.dtype == kDtypeFp32) static_cast<float*>(p.out)[at] = sum;
+                    else if (p.dtype == kDtypeBf16) static_cast<bf16*>(p.out)[at] = __float2bfloat16_rn(sum);
+                    else static_cast<__half*>(p.out)[at] = __float2half_rn(sum);
+                }
+            }
+        }
+        ptx::cluster_sync_all();   // no rank leaves while its sums are read
+    }
     if (warp == 2) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, C::kTmemCols);

@@ -17,59 +17,89 @@ int sms_of(int dev) {
     return n;
 }
 
-// Shared memory of `kern` raised to `bytes`, once per kernel (its flags `set`) and device.
-template <class K>
-cudaError_t allow_smem(K kern, int bytes, bool* set, int dev) {
-    if (dev >= 0 && dev < kMaxDevices && set[dev]) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) set[dev] = true;
-    return e;
+// How k_fp8_few splits `tiles` tiles of kb blocks: as far as every cluster is resident at once
+// and each CTA has two blocks or more. clusters[i]: resident clusters of 2^i CTAs.
+int few_split(long long tiles, int kb, const int (&clusters)[4]) {
+    int i = 0;
+    while (i < 3 && tiles <= clusters[i + 1] && kb >= 4 << i) ++i;
+    return 1 << i;
+}
+
+// What the host knows of one width of k_fp8_few on a device: resident clusters of 1, 2, 4 and 8 CTAs.
+struct FewDevice {
+    int clusters[4];
+    bool known;
+};
+
+template <int BN>
+cudaError_t few_device(int dev, FewDevice* out) {
+    static FewDevice cached[kMaxDevices] = {};
+    const bool keep = dev >= 0 && dev < kMaxDevices;
+    if (keep && cached[dev].known) {
+        *out = cached[dev];
+        return cudaSuccess;
+    }
+    cudaError_t e = cudaFuncSetAttribute(fp8::k_fp8_few<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         fp8::FewCfg<BN>::kSmem);
+    if (e != cudaSuccess) return e;
+    FewDevice d{{sms_of(dev), 0, 0, 0}, true};
+    for (int i = 1; i < 4; ++i) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(sms_of(dev) / 8 * 8);
+        cfg.blockDim = dim3(fp8::kFewThreads);
+        cfg.dynamicSmemBytes = fp8::FewCfg<BN>::kSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 1 << i;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&d.clusters[i], fp8::k_fp8_few<BN>, &cfg);
+        if (e != cudaSuccess) return e;
+    }
+    if (keep) cached[dev] = d;
+    *out = d;
+    return cudaSuccess;
 }
 
 template <int BN>
-cudaError_t launch_few(const void* x, const void* w, const fp8::Problem& p, cudaStream_t s) {
+cudaError_t launch_few(const void* x, const void* w, const fp8::Problem& p, int dev, cudaStream_t s) {
     using C = fp8::FewCfg<BN>;
-    auto kern = fp8::k_fp8_few<BN>;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    static bool attr_set[kMaxDevices] = {};
-    e = allow_smem(kern, C::kSmem, attr_set, dev);
+    FewDevice fd;
+    const cudaError_t e = few_device<BN>(dev, &fd);
     if (e != cudaSuccess) return e;
     CUtensorMap tw, tx;
     if (!make_tma_2d(&tw, w, (uint64_t)p.k, (uint64_t)p.groups * p.n, (uint64_t)p.k, fp8::BK, fp8::BF, 128, 1) ||
         !make_tma_2d(&tx, x, (uint64_t)p.k, (uint64_t)p.rows, (uint64_t)p.k, fp8::BK, BN, 128, 1))
         return cudaErrorInvalidValue;
     // Tiles there can be: a row tile for every BN rows and one more for each group that has rows.
-    const int sms = sms_of(dev), f_tiles = (p.n + fp8::BF - 1) / fp8::BF;
-    const long long tiles = ((long long)(p.rows - 1) / BN + std::min(p.groups, p.rows)) * f_tiles;
-    // Few tiles leave SMs idle and a long chain of K blocks to each: split K as far as the SMs
-    // and at least two blocks a CTA go.
+    const long long tiles = ((long long)(p.rows - 1) / BN + std::min(p.groups, p.rows)) * ((p.n + fp8::BF - 1) / fp8::BF);
     fp8::Problem q = p;
-    while (q.split < 8 && tiles * q.split * 2 <= sms && p.kb >= 4 * q.split) q.split *= 2;
-    const int grid = (int)std::min<long long>(tiles, sms) * q.split;
+    q.split = few_split(tiles, p.kb, fd.clusters);
+    const dim3 grid((unsigned)std::min<long long>(tiles, sms_of(dev)) * q.split), block(fp8::kFewThreads);
+    if (q.split == 1) return launch_pdl(fp8::k_fp8_few<BN>, grid, block, C::kSmem, s, tw, tx, q);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(fp8::kFewThreads);
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
-    if (q.split == 1) return launch_pdl(kern, dim3(grid), dim3(fp8::kFewThreads), C::kSmem, s, tw, tx, q);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = q.split;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, tw, tx, q);
+    return cudaLaunchKernelEx(&cfg, fp8::k_fp8_few<BN>, tw, tx, q);
 }
 
-cudaError_t launch_many(const void* x, const void* w, const fp8::Problem& p, cudaStream_t s) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
+cudaError_t launch_many(const void* x, const void* w, const fp8::Problem& p, int dev, cudaStream_t s) {
     static bool attr_set[kMaxDevices] = {};
-    e = allow_smem(fp8::k_fp8_many, fp8::kManySmem, attr_set, dev);
-    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices || !attr_set[dev]) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(fp8::k_fp8_many, cudaFuncAttributeMaxDynamicSharedMemorySize, fp8::kManySmem);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < kMaxDevices) attr_set[dev] = true;
+    }
     CUtensorMap tx, tw;
     if (!make_tma_2d(&tx, x, (uint64_t)p.k, (uint64_t)p.rows, (uint64_t)p.k, fp8::BK, fp8::kManyRows, 128, 1) ||
         !make_tma_2d(&tw, w, (uint64_t)p.k, (uint64_t)p.groups * p.n, (uint64_t)p.k, fp8::BK, fp8::kManyFeatures / 2, 128, 1))
@@ -79,6 +109,52 @@ cudaError_t launch_many(const void* x, const void* w, const fp8::Problem& p, cud
                             ((p.n + fp8::kManyFeatures - 1) / fp8::kManyFeatures);
     const int pairs = (int)std::min<long long>(tiles, std::max(1, sms_of(dev) / 2));
     return launch_pdl(fp8::k_fp8_many, dim3(2 * pairs), dim3(fp8::kManyThreads), fp8::kManySmem, s, tx, tw, p);
+}
+
+// Estimated time of the plain product by k_fp8_few<BN>, in 10 ns: `block` for each K block of a
+// tile, and 6 us around them.
+template <int BN>
+cudaError_t few_cost(const fp8::Problem& p, int dev, int block, long long* cost) {
+    FewDevice fd;
+    const cudaError_t e = few_device<BN>(dev, &fd);
+    if (e != cudaSuccess) return e;
+    const long long tiles = ((long long)p.rows + BN - 1) / BN * ((p.n + fp8::BF - 1) / fp8::BF);
+    const int split = few_split(tiles, p.kb, fd.clusters), sms = sms_of(dev);
+    *cost = 600 + block * ((tiles + sms - 1) / sms) * ((p.kb + split - 1) / split);
+    return cudaSuccess;
+}
+
+// Which kernel and width (k_fp8_few's rows a tile, or 0 for k_fp8_many). Measured a K block of a
+// CTA's tile: 0.30, 0.32, 0.36 and 0.66 us for 128 features x 16, 32, 64 and 128 rows, 0.55 us for
+// a pair's 256 x 256. The plain product's tiles are known, so the estimates are compared
+// (measured, us, few of 16 / 32 / 64 / 128 / many, K = 7168: 16 x 7168 15.6 / 16.3 / 17.3 / 21.1 /
+// 35.2, 128 x 1536 22 / 17 / 13.7 / 12.8 / 34.8, 256 x 7168 120 / 74 / 45 / 34.8 / 33.5,
+// 512 x 1536 55 / 40 / 25 / 27 / 33). Of groups only the rows' capacity is known, so it goes by
+// the average (32 experts, N = 4096, K = 7168: 8 rows 141 / 143 / 151 / 198 / 249, 32 rows
+// 355 / 222 / 197 / 244 / 251, 64 rows 544 / 353 / 220 / 243 / 252, 96 rows 799 / 471 / 293 / 286 / 253);
+// at 17 to 32 the narrower tile, since a rank that holds a share of the experts has fewer rows than
+// capacity (4 rows at a capacity of 32: 142 against 151).
+cudaError_t choose(const fp8::Problem& p, int dev, int* width) {
+    if (p.offsets) {
+        const long long g = p.groups;
+        *width = p.rows <= 8 * g ? 16 : p.rows <= 32 * g ? 32 : p.rows <= 64 * g ? 64 : 0;
+        return cudaSuccess;
+    }
+    const long long pairs = std::max(1, sms_of(dev) / 2);
+    const long long tiles = ((long long)p.rows + 2 * fp8::kManyRows - 1) / (2 * fp8::kManyRows) *
+                            ((p.n + fp8::kManyFeatures - 1) / fp8::kManyFeatures);
+    long long best = 400 + 55 * ((tiles + pairs - 1) / pairs) * p.kb, c[4];
+    cudaError_t e = few_cost<16>(p, dev, 30, &c[0]);
+    if (e == cudaSuccess) e = few_cost<32>(p, dev, 32, &c[1]);
+    if (e == cudaSuccess) e = few_cost<64>(p, dev, 36, &c[2]);
+    if (e == cudaSuccess) e = few_cost<128>(p, dev, 66, &c[3]);
+    *width = 0;
+    for (int i = 0; i < 4; ++i)
+        if (c[i] < best) {
+            best = c[i];
+            *width = 16 << i;
+        }
+    return e;
 }
 
 }  // namespace
@@ -92,12 +168,19 @@ cudaError_t launch_fp8_gemm(const void* x, const float* xs, const void* w, const
                             int rows, int groups, int n, int k, void* out, int dtype, int32_t* status,
                             cudaStream_t s) {
     fp8::Problem p{xs, ws, offsets, rows, groups, n, k, (n + 127) / 128, (k + 127) / 128, out, dtype, status, 1};
-    const long long per_group = ((long long)rows + groups - 1) / groups;
-    if (per_group <= 16) return launch_few<16>(x, w, p, s);
-    if (per_group <= 32) return launch_few<32>(x, w, p, s);
-    if (per_group <= 64) return launch_few<64>(x, w, p, s);
-    if (per_group <= 128) return launch_few<128>(x, w, p, s);
-    return launch_many(x, w, p, s);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int width = 0;
+    e = choose(p, dev, &width);
+    if (e != cudaSuccess) return e;
+    switch (width) {
+        case 16: return launch_few<16>(x, w, p, dev, s);
+        case 32: return launch_few<32>(x, w, p, dev, s);
+        case 64: return launch_few<64>(x, w, p, dev, s);
+        case 128: return launch_few<128>(x, w, p, dev, s);
+        default: return launch_many(x, w, p, dev, s);
+    }
 }
 
 }  // namespace mla

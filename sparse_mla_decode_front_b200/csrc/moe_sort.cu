@@ -26,7 +26,6 @@ constexpr int kPerLane = 4;                            // choices a lane holds i
 constexpr int kPassItems = kThreads * kPerLane;        // choices of one pass of a block
 constexpr int kSingleItems = kPassItems;
 constexpr int kMaxChunks = 256;                        // chunks (blocks) of the two-launch form
-constexpr int kWeightTokens = kThreads;                // tokens of one weight block
 constexpr unsigned kAll = 0xffffffffu;
 
 struct Args {
@@ -45,35 +44,23 @@ __device__ __forceinline__ int key_of(const Args& a, int i) {
     return (unsigned)e < (unsigned)a.E ? e : a.E;
 }
 
-// Routing weights of the tokens of block `b` of the weight blocks, one token a thread.
+// Routing weights of the tokens of block `b` of the weight blocks: a lane for each choice, so
+// that the choices are read and the weights written side by side, 32 / K whole tokens a warp; a
+// token's sum is taken in the order of its choices.
 __device__ void token_weights(const Args& a, int b) {
-    const int t = b * kWeightTokens + threadIdx.x;
-    if (t >= a.T) return;
-    const int32_t* idx = a.idx + (size_t)t * a.K;
-    const bf16* aff = a.aff + (size_t)t * a.n_total;
-    float v[8];
-    float sum = 0.f;
-    for (int k0 = 0; k0 < a.K; k0 += 8) {   // eight loads in flight
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int e = k0 + j < a.K ? idx[k0 + j] : -1;
-            v[j] = (unsigned)e < (unsigned)a.n_total ? bf2f(aff[e]) : 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum += v[j];
+    const int lane = threadIdx.x & 31, per_warp = 32 / a.K, g = lane / a.K;
+    const long long t = ((long long)b * kWarps + (threadIdx.x >> 5)) * per_warp + g;
+    const bool on = g < per_warp && t < a.T;
+    const long long c = t * a.K + (lane - g * a.K);
+    const int e = on ? a.idx[c] : -1;
+    const float v = (unsigned)e < (unsigned)a.n_total ? bf2f(a.aff[(size_t)t * a.n_total + e]) : 0.f;
+    float w = v;
+    if (a.normalize) {
+        float sum = 0.f;
+        for (int j = 0; j < a.K; ++j) sum += __shfl_sync(kAll, v, min(g * a.K + j, 31));
+        w = sum == 0.f ? 0.f : v / sum;
     }
-    for (int k0 = 0; k0 < a.K; k0 += 8) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (k0 + j >= a.K) break;
-            if (a.K > 8) {   // more than one group: read again (cached)
-                const int e = idx[k0 + j];
-                v[j] = (unsigned)e < (unsigned)a.n_total ? bf2f(aff[e]) : 0.f;
-            }
-            const float w = !a.normalize ? v[j] : sum == 0.f ? 0.f : v[j] / sum;
-            a.weights[(size_t)t * a.K + k0 + j] = a.scale * w;
-        }
-    }
+    if (on) a.weights[c] = a.scale * w;
 }
 
 // Exclusive prefix sum of v over the block's threads; `red` holds kWarps ints.
@@ -118,18 +105,21 @@ __device__ void bin_bases(const int* total, int* base, int bins, int* red) {
     }
 }
 
-// Place up to kPassItems choices [i0, i1): base[] holds each bin's next row and is advanced.
-// `single`: base[] is computed here from this pass's own counts (the whole input), and the
-// offsets are written. cnt: [kWarps][bins] uint16 counts, total / base: [bins].
-__device__ void place_pass(const Args& a, int i0, int i1, uint16_t* cnt, int* total, int* base, int* red,
-                           bool single) {
+// Count up to kPassItems choices [i0, i1): each choice's place within its warp, the warps'
+// counts turned into those of the warps before (cnt [kWarps][bins]) and the bins' sums (total).
+struct Pass {
+    int w0, groups;                       // the warp's first choice, its groups of 32
+    int key[kPerLane], place[kPerLane];   // bin (-1: none), place among the warp's choices of the bin
+};
+__device__ void count_pass(const Args& a, Pass& s, int i0, int i1, uint16_t* cnt, int* total) {
     const int bins = a.E + 1, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    int key[kPerLane], place[kPerLane];
-    const int w0 = i0 + wid * (32 * kPerLane);
+    int (&key)[kPerLane] = s.key, (&place)[kPerLane] = s.place;
+    s.groups = min(kPerLane, (i1 - i0 + kThreads - 1) / kThreads);   // a short pass still takes all warps
+    s.w0 = i0 + wid * (32 * s.groups);
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) {
-        const int i = w0 + 32 * j + lane;
-        key[j] = i < i1 ? key_of(a, i) : -1;
+        const int i = s.w0 + 32 * j + lane;
+        key[j] = j < s.groups && i < i1 ? key_of(a, i) : -1;
     }
     uint32_t* cw = reinterpret_cast<uint32_t*>(cnt);
     for (int b = threadIdx.x; b < (kWarps * bins + 1) / 2; b += kThreads) cw[b] = 0;
@@ -137,6 +127,7 @@ __device__ void place_pass(const Args& a, int i0, int i1, uint16_t* cnt, int* to
     uint16_t* mine = cnt + wid * bins;
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) {
+        if (j >= s.groups) break;
         const unsigned same = __match_any_sync(kAll, key[j]);
         const unsigned before = same & ((1u << lane) - 1);
         place[j] = 0;
@@ -148,38 +139,35 @@ __device__ void place_pass(const Args& a, int i0, int i1, uint16_t* cnt, int* to
     __syncthreads();
     // counts -> counts of the warps before; a bin's sum over all warps to total[]
     for (int b = threadIdx.x; b < bins; b += kThreads) {
-        int s = 0;
+        int t = 0;
 #pragma unroll 8
         for (int w = 0; w < kWarps; ++w) {
             const int c = cnt[w * bins + b];
-            cnt[w * bins + b] = (uint16_t)s;
-            s += c;
+            cnt[w * bins + b] = (uint16_t)t;
+            t += c;
         }
-        total[b] = s;
+        total[b] = t;
     }
     __syncthreads();
-    if (single) {
-        bin_bases(total, base, bins, red);
-        for (int b = threadIdx.x; b < bins; b += kThreads) a.offsets[b] = base[b];
-    }
+}
+
+// Rows of a counted pass: base[] holds each bin's next row.
+__device__ __forceinline__ void write_pass(const Args& a, const Pass& s, const uint16_t* cnt, const int* base) {
+    const uint16_t* mine = cnt + (threadIdx.x >> 5) * (a.E + 1);
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) {
-        if (key[j] < 0) continue;
-        const int i = w0 + 32 * j + lane;
-        const int row = base[key[j]] + mine[key[j]] + place[j];
-        const bool here = key[j] < a.E;
+        const int k = s.key[j];
+        if (k < 0) continue;
+        const int i = s.w0 + 32 * j + (threadIdx.x & 31);
+        const int row = base[k] + mine[k] + s.place[j];
+        const bool here = k < a.E;
         a.row_of[i] = here ? row : -1;
         a.source_of[row] = here ? i : -1;   // the last bin's rows lie behind the last expert's
     }
-    if (!single) {
-        __syncthreads();
-        for (int b = threadIdx.x; b < bins; b += kThreads) base[b] += total[b];
-        __syncthreads();
-    }
 }
 
-// Shared memory: total and base [bins], then the warps' counts.
-size_t smem_bytes(int bins) { return sizeof(int) * 2 * bins + sizeof(uint16_t) * (kWarps * bins + 1) + 4; }
+// Shared memory: `arrays` of [bins] int32, then the warps' counts.
+size_t smem_bytes(int arrays, int bins) { return sizeof(int) * arrays * bins + sizeof(uint16_t) * (kWarps * bins + 1) + 4; }
 
 __global__ void __launch_bounds__(kThreads) k_moe_sort_single(Args a) {
     extern __shared__ int sm[];
@@ -191,14 +179,21 @@ __global__ void __launch_bounds__(kThreads) k_moe_sort_single(Args a) {
         return;
     }
     const int bins = a.E + 1;
-    place_pass(a, 0, a.n, reinterpret_cast<uint16_t*>(sm + 2 * bins), sm, sm + bins, red, true);
+    int *total = sm, *base = sm + bins;
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(sm + 2 * bins);
+    Pass s;
+    count_pass(a, s, 0, a.n, cnt, total);
+    bin_bases(total, base, bins, red);
+    for (int b = threadIdx.x; b < bins; b += kThreads) a.offsets[b] = base[b];
+    write_pass(a, s, cnt, base);
 }
 
-// First launch: blocks [0, chunks) count their chunk's bins, the others weigh tokens.
+// First launch: blocks [0, chunks) count their chunk's bins, the others weigh tokens. The
+// second launch may start once every block here is past its wait (see k_moe_sort_place).
 __global__ void __launch_bounds__(kThreads) k_moe_sort_count(Args a) {
     extern __shared__ int sm[];
-    griddep_launch();
     griddep_wait();
+    griddep_launch();
     if ((int)blockIdx.x >= a.chunks) {
         token_weights(a, blockIdx.x - a.chunks);
         return;
@@ -208,50 +203,66 @@ __global__ void __launch_bounds__(kThreads) k_moe_sort_count(Args a) {
     __syncthreads();
     const int i0 = blockIdx.x * a.chunk_items;                   // < n, so no overflow
     const int len = min(a.chunk_items, a.n - i0);
-    for (int i = threadIdx.x; i < len; i += kThreads) atomicAdd(sm + key_of(a, i0 + i), 1);   // whole numbers: any order
+    int none = 0;   // choices without a row here, often most of them: counted apart from the atomics
+#pragma unroll 4
+    for (int i = threadIdx.x; i < len; i += kThreads) {
+        const int k = key_of(a, i0 + i);
+        if (k < a.E) atomicAdd(sm + k, 1);   // whole numbers: any order
+        else ++none;
+    }
+    none = __reduce_add_sync(kAll, none);
+    if ((threadIdx.x & 31) == 0 && none > 0) atomicAdd(sm + a.E, none);
     __syncthreads();
     for (int b = threadIdx.x; b < bins; b += kThreads) a.hist[(size_t)blockIdx.x * bins + b] = sm[b];
 }
 
 // Second launch: each block's bases are the bins before plus the same bin of the chunks before.
+// The first pass is counted before the wait for the first launch: it reads the choices alone,
+// which were complete before that launch let this one start.
 __global__ void __launch_bounds__(kThreads) k_moe_sort_place(Args a) {
     extern __shared__ int sm[];
     __shared__ int red[kWarps];
     griddep_launch();
-    griddep_wait();
     const int bins = a.E + 1;
-    int *total = sm, *base = sm + bins;
-    uint16_t* cnt = reinterpret_cast<uint16_t*>(sm + 2 * bins);
-    int* before = reinterpret_cast<int*>(cnt);   // [bins], until the first pass
-    for (int b = threadIdx.x; b < bins; b += kThreads) total[b] = before[b] = 0;
-    __syncthreads();
+    int *total = sm, *base = sm + bins, *all = sm + 2 * bins, *before = sm + 3 * bins;
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(sm + 4 * bins);
+    const int c0 = blockIdx.x * a.chunk_items;
+    const int len = min(a.chunk_items, a.n - c0);
+    for (int b = threadIdx.x; b < bins; b += kThreads) all[b] = before[b] = 0;
+    Pass s;
+    count_pass(a, s, c0, c0 + min(len, kPassItems), cnt, total);
+    griddep_wait();
     // several threads share a bin where there are few bins
     const int teams = max(1, kThreads / bins);
     const int team = threadIdx.x / bins, b1 = threadIdx.x - team * bins;
     for (int b = bins <= kThreads ? (team < teams ? b1 : bins) : threadIdx.x; b < bins;
          b += bins <= kThreads ? bins : kThreads) {
-        int all = 0, prev = 0;
+        int sum = 0, prev = 0;
         const int t0 = bins <= kThreads ? team : 0, step = bins <= kThreads ? teams : 1;
 #pragma unroll 4
         for (int c = t0; c < a.chunks; c += step) {
-            const int h = __ldcg(a.hist + (size_t)c * bins + b);
-            all += h;
+            const int h = a.hist[(size_t)c * bins + b];
+            sum += h;
             prev += c < (int)blockIdx.x ? h : 0;
         }
-        atomicAdd(total + b, all);
-        atomicAdd(before + b, prev);
+        if (sum) atomicAdd(all + b, sum);
+        if (prev) atomicAdd(before + b, prev);
     }
     __syncthreads();
-    bin_bases(total, base, bins, red);
+    bin_bases(all, base, bins, red);
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < bins; b += kThreads) a.offsets[b] = base[b];
     __syncthreads();
     for (int b = threadIdx.x; b < bins; b += kThreads) base[b] += before[b];
     __syncthreads();
-    const int c0 = blockIdx.x * a.chunk_items;
-    const int len = min(a.chunk_items, a.n - c0);
-    for (int o = 0; o < len; o += kPassItems)
-        place_pass(a, c0 + o, c0 + min(len, o + kPassItems), cnt, total, base, red, false);
+    write_pass(a, s, cnt, base);
+    for (int o = kPassItems; o < len; o += kPassItems) {
+        __syncthreads();
+        for (int b = threadIdx.x; b < bins; b += kThreads) base[b] += total[b];
+        __syncthreads();
+        count_pass(a, s, c0 + o, c0 + min(len, o + kPassItems), cnt, total);
+        write_pass(a, s, cnt, base);
+    }
 }
 
 // Chunks of whole passes, at most kMaxChunks of them.
@@ -284,8 +295,9 @@ cudaError_t launch_moe_sort(const int32_t* idx, const bf16* aff, int T, int K, i
     if (T == 0) return cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (E + 1), s);
     Args a{idx, aff, T, K, n_total, first, E, normalize, scale, offsets, row_of, source_of, weights,
            static_cast<int32_t*>(workspace), T * K, 1, 0};
-    const int weight_blocks = aff ? (T + kWeightTokens - 1) / kWeightTokens : 0;
-    const size_t smem = smem_bytes(E + 1);
+    const int weight_tokens = kWarps * (32 / K);   // of one block
+    const int weight_blocks = aff ? (T + weight_tokens - 1) / weight_tokens : 0;
+    const size_t smem = smem_bytes(2, E + 1), smem_place = smem_bytes(4, E + 1);
     if (a.n <= kSingleItems) {
         cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_moe_sort_single), smem);
         if (e != cudaSuccess) return e;
@@ -295,9 +307,9 @@ cudaError_t launch_moe_sort(const int32_t* idx, const bf16* aff, int T, int K, i
     cudaError_t e = launch_pdl(k_moe_sort_count, dim3(a.chunks + weight_blocks), dim3(kThreads),
                                sizeof(int) * (E + 1), s, a);
     if (e != cudaSuccess) return e;
-    e = allow_smem(reinterpret_cast<const void*>(k_moe_sort_place), smem);
+    e = allow_smem(reinterpret_cast<const void*>(k_moe_sort_place), smem_place);
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_moe_sort_place, dim3(a.chunks), dim3(kThreads), smem, s, a);
+    return launch_pdl_mode(true, k_moe_sort_place, dim3(a.chunks), dim3(kThreads), smem_place, s, a);
 }
 
 }  // namespace mla

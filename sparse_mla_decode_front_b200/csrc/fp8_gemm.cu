@@ -17,6 +17,28 @@ int sms_of(int dev) {
     return n;
 }
 
+// launch_pdl (common.cuh) in clusters of `size` CTAs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), int size, dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                           Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) cap = cudaStreamCaptureStatusNone;
+    cfg.attrs = attr;
+    cfg.numAttrs = cap == cudaStreamCaptureStatusNone ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
 // How k_fp8_few splits `tiles` tiles of kb blocks: as far as every cluster is resident at once
 // and each CTA has two blocks or more. clusters[i]: resident clusters of 2^i CTAs.
 int few_split(long long tiles, int kb, const int (&clusters)[4]) {
@@ -78,37 +100,31 @@ cudaError_t launch_few(const void* x, const void* w, const fp8::Problem& p, int 
     q.split = few_split(tiles, p.kb, fd.clusters);
     const dim3 grid((unsigned)std::min<long long>(tiles, sms_of(dev)) * q.split), block(fp8::kFewThreads);
     if (q.split == 1) return launch_pdl(fp8::k_fp8_few<BN>, grid, block, C::kSmem, s, tw, tx, q);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = q.split;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fp8::k_fp8_few<BN>, tw, tx, q);
+    return launch_cluster(fp8::k_fp8_few<BN>, q.split, grid, block, C::kSmem, s, tw, tx, q);
 }
 
+template <bool PAIR>
 cudaError_t launch_many(const void* x, const void* w, const fp8::Problem& p, int dev, cudaStream_t s) {
+    using C = fp8::ManyCfg<PAIR>;
     static bool attr_set[kMaxDevices] = {};
     if (dev < 0 || dev >= kMaxDevices || !attr_set[dev]) {
         const cudaError_t e =
-            cudaFuncSetAttribute(fp8::k_fp8_many, cudaFuncAttributeMaxDynamicSharedMemorySize, fp8::kManySmem);
+            cudaFuncSetAttribute(fp8::k_fp8_many<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDevices) attr_set[dev] = true;
     }
     CUtensorMap tx, tw;
     if (!make_tma_2d(&tx, x, (uint64_t)p.k, (uint64_t)p.rows, (uint64_t)p.k, fp8::BK, fp8::kManyRows, 128, 1) ||
-        !make_tma_2d(&tw, w, (uint64_t)p.k, (uint64_t)p.groups * p.n, (uint64_t)p.k, fp8::BK, fp8::kManyFeatures / 2, 128, 1))
+        !make_tma_2d(&tw, w, (uint64_t)p.k, (uint64_t)p.groups * p.n, (uint64_t)p.k, fp8::BK, C::kWRows, 128, 1))
         return cudaErrorInvalidValue;
-    const int rows = 2 * fp8::kManyRows;
-    const long long tiles = (((long long)p.rows + rows - 1) / rows + p.groups - 1) *
+    const long long tiles = ((long long)(p.rows - 1) / C::kRows + std::min(p.groups, p.rows)) *
                             ((p.n + fp8::kManyFeatures - 1) / fp8::kManyFeatures);
-    const int pairs = (int)std::min<long long>(tiles, std::max(1, sms_of(dev) / 2));
-    return launch_pdl(fp8::k_fp8_many, dim3(2 * pairs), dim3(fp8::kManyThreads), fp8::kManySmem, s, tx, tw, p);
+    if (!PAIR)
+        return launch_pdl(fp8::k_fp8_many<PAIR>, dim3((unsigned)std::min<long long>(tiles, sms_of(dev))),
+                          dim3(fp8::kManyThreads), C::kSmem, s, tx, tw, p);
+    const long long pairs = std::min<long long>(tiles, std::max(1, sms_of(dev) / 2));
+    return launch_cluster(fp8::k_fp8_many<PAIR>, 2, dim3((unsigned)(2 * pairs)), dim3(fp8::kManyThreads), C::kSmem, s, tx,
+                          tw, p);
 }
 
 // Estimated time of the plain product by k_fp8_few<BN>, in 10 ns: `block` for each K block of a
@@ -179,7 +195,7 @@ cudaError_t launch_fp8_gemm(const void* x, const float* xs, const void* w, const
         case 32: return launch_few<32>(x, w, p, dev, s);
         case 64: return launch_few<64>(x, w, p, dev, s);
         case 128: return launch_few<128>(x, w, p, dev, s);
-        default: return launch_many(x, w, p, dev, s);
+        default: return offsets ? launch_many<false>(x, w, p, dev, s) : launch_many<true>(x, w, p, dev, s);
     }
 }
 

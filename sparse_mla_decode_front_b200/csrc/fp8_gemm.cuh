@@ -54,14 +54,24 @@ struct Problem {
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
+// PAIR: issued by the leader of a CTA pair, for both.
+template <bool PAIR = false>
 __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                           uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
 }
 
 // The tiles of all groups: group g has rows [bound[g], bound[g + 1]) and tiles
@@ -136,30 +146,37 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     return v;
 }
 
-// The UMMAs of every second K block of the CTA, from block `first` on; total: all its tiles'
-// blocks. One thread needs about 870 clocks a block (two waits of about 120, four UMMAs, two
-// commits of about 75, each of which it sits out; measured on the 128 x 256 tile), more than
-// the 512 that the tensor cores need. The blocks' accumulators are independent, so two
-// threads of different warps take turns: 1.4 to 2 times the rate. `issue(stage, buf)` issues
-// one block's. Past K both operands are zero-filled, so a partial last block has no other form.
-template <int S, int BUFS, class F>
-__device__ __forceinline__ bool issue_blocks(int first, long long total, uint64_t* full_bar, uint64_t* empty_bar,
-                                             uint64_t* acc_full, uint64_t* acc_empty, int32_t* status, F issue) {
+// The UMMAs of every second K block, from block `first` on, of `tiles` tiles of `kb` blocks.
+// One thread needs about 870 clocks a block (two waits of about 120, four UMMAs, two commits
+// of about 75, each of which it sits out; measured on a 128 x 256 tile), more than the 512
+// that the tensor cores need. The blocks' accumulators are independent, so two threads of
+// different warps take turns: 1.4 to 2 times the rate. idesc_of(i): the instruction
+// descriptor of tile i; issue(idesc, stage, buf): one block's UMMAs; commit(bar). Past K both
+// operands are zero-filled, so a partial last block has no other form.
+template <int S, int BUFS, class D, class F, class C>
+__device__ __forceinline__ bool issue_blocks(int first, int tiles, int kb, uint64_t* full_bar, uint64_t* empty_bar,
+                                             uint64_t* acc_full, uint64_t* acc_empty, int32_t* status, D idesc_of,
+                                             F issue, C commit) {
     static_assert(S >= 2 && BUFS % 2 == 0, "each issuer has its own accumulators");
     int stage = first, buf = first;
     uint32_t phase = 0, buf_phase = 0;
-    for (long long i = first; i < total; i += 2) {
-        if (!ptx::mbar_wait(&full_bar[stage], phase, status) ||
-            !ptx::mbar_wait(&acc_empty[buf], buf_phase ^ 1, status))
-            return false;
-        ptx::tc_fence_after();
-        issue(stage, buf);
-        ptx::umma_commit(&acc_full[buf]);
-        ptx::umma_commit(&empty_bar[stage]);
-        stage += 2;
-        if (stage >= S) { stage -= S; phase ^= 1; }
-        buf += 2;
-        if (buf >= BUFS) { buf -= BUFS; buf_phase ^= 1; }
+    int next = first;   // block of the tile
+    for (int i = 0; i < tiles; ++i) {
+        const uint32_t idesc = idesc_of(i);
+        for (; next < kb; next += 2) {
+            if (!ptx::mbar_wait(&full_bar[stage], phase, status) ||
+                !ptx::mbar_wait(&acc_empty[buf], buf_phase ^ 1, status))
+                return false;
+            ptx::tc_fence_after();
+            issue(idesc, stage, buf);
+            commit(&acc_full[buf]);
+            commit(&empty_bar[stage]);
+            stage += 2;
+            if (stage >= S) { stage -= S; phase ^= 1; }
+            buf += 2;
+            if (buf >= BUFS) { buf -= BUFS; buf_phase ^= 1; }
+        }
+        next -= kb;
     }
     return true;
 }
@@ -250,15 +267,18 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
     } else if ((warp == 1 || warp == kFewIssuer2) && lane == 0) {
         // ---------------- UMMA, two issuers (see issue_blocks)
         constexpr uint32_t idesc = idesc_e4m3(BF, BN);
-        const bool ok = issue_blocks<S, kBufs>(warp == 1 ? 0 : 1, (long long)my_tiles(tiles, t0, t_step) * (kb1 - kb0), full_bar, empty_bar,
-                                              acc_full, acc_empty, p.status, [&](int stage, int buf) {
-            const uint32_t w_addr = ptx::smem_u32(smem + stage * C::kStageBytes);
-            const uint64_t wd = ptx::sdesc_sw128(w_addr, 16, 1024);
-            const uint64_t xd = ptx::sdesc_sw128(w_addr + C::kWBytes, 16, 1024);
+        const bool ok = issue_blocks<S, kBufs>(
+            warp == 1 ? 0 : 1, my_tiles(tiles, t0, t_step), kb1 - kb0, full_bar, empty_bar, acc_full, acc_empty, p.status,
+            [&](int) { return idesc; },
+            [&](uint32_t, int stage, int buf) {
+                const uint32_t w_addr = ptx::smem_u32(smem + stage * C::kStageBytes);
+                const uint64_t wd = ptx::sdesc_sw128(w_addr, 16, 1024);
+                const uint64_t xd = ptx::sdesc_sw128(w_addr + C::kWBytes, 16, 1024);
 #pragma unroll
-            for (int kk = 0; kk < BK / 32; ++kk)   // K = 32 further: 32 bytes, 2 in the descriptor's units
-                umma_e4m3(tmem + buf * BN, wd + 2 * kk, xd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
-        });
+                for (int kk = 0; kk < BK / 32; ++kk)   // K = 32 further: 32 bytes, 2 in the descriptor's units
+                    umma_e4m3(tmem + buf * BN, wd + 2 * kk, xd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+            },
+            [](uint64_t* bar) { ptx::umma_commit(bar); });
         if (!ok) abort_flag = 1;
         ptx::umma_commit(&mma_done);   // all UMMAs complete before TMEM is released
         ptx::mbar_wait(&mma_done, 0, p.status);
@@ -437,31 +457,44 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
 }
 
 // ------------------------------------------------------------------ many rows per group
-// k_fp8_many: a pair of CTAs on a tile of 256 rows x 256 features, the rows as the UMMA's A
-// operand (cta_group::2, M = 256: each CTA holds 128 rows of x, the weight rows are split
-// between the two, and each CTA's tensor core reads both halves). TMEM lane = row, so a drain
-// thread needs one scale per block and not one per column.
+// k_fp8_many<PAIR>: tiles of 128 rows a CTA x 256 features, the rows as the UMMA's A operand.
+// TMEM lane = row, so a drain thread needs one scale per block and not one per column; it holds
+// the fp32 sums of 128 columns in registers (setmaxnreg moves the other warps' to it), and two
+// accumulators of 256 columns take turns.
 //
-// Why a pair: a block of a 128 x 256 tile of one CTA takes 48 KB of operands for 512 tensor
-// clocks, and an SM takes in about 64 bytes a clock from L2 (390 ns a block measured with the
-// drain left out: 62 bytes a clock); the pair needs 32 KB a CTA. Why sixteen drain warps: the
-// drain of a block is a chain of waits (for the accumulator, for TMEM loads) and 256 issue
-// slots of additions on each scheduler; four warps of 64 columns each on a scheduler hide one
-// another's waits, which two of 128 columns did not (1235 clocks a block).
+// PAIR: two CTAs share a tile of 256 rows (cta_group::2, M = 256: each holds 128 rows of x and
+// half of the weight rows, and each one's tensor core reads both halves). A block then takes
+// 32 KB of operands a CTA instead of 48, and an SM takes in about 64 bytes a clock from L2
+// (390 ns a block measured for the single CTA with the drain left out). Measured in a loop (the
+// 1000 W cap holds the clock at 1.54 GHz): 4096 x 7168 x 16384 530 us, 1.8 PFLOP/s, against 579 us
+// for single CTAs. But a group's last tile is half empty on average, and of 128 rows that costs less
+// than of 256: 8191 rows over 32 experts (3 to 2156 each), 4096 x 7168: 369 - 441 us single, 439 - 480
+// us in pairs. Hence pairs for the plain product, single CTAs for groups.
 //
-// Warps 0-3 (32 registers): 0 TMA, 1 and 2 UMMA (leader only; every second block each, see
-// issue_blocks), 3 scales and TMEM. Warps 4-19 (112 registers): the drain, four warps to 64
-// columns, the fp32 sums in each thread's registers.
+// What bounds it: 0.52 us a block of a CTA (1.965 GHz) against 0.26 for the tensor cores alone.
+// Loads, products and hand-overs without any drain take 0.44. The drain is a chain: a wait for
+// the accumulator (about 75 clocks), TMEM reads of 32 columns overlapped with the additions of
+// the 32 before (4 x 90), the hand-back; two warps a scheduler fill each other's gaps. Tried and
+// slower: accumulators of 128 columns with four issuing threads (+24%), 16 drain warps of 64
+// columns (+22%), packed fp32 pairs (+8%: moves), column counts that are not compile-time (+25%).
+//
+// Warps 0-3 (72 registers): 0 TMA, 1 and 2 UMMA (every second block each, see issue_blocks; of a
+// pair the leader's only), 3 scales and TMEM. Warps 4-11 (216 registers): the drain, four warps
+// to 128 columns.
 constexpr int kManyThreads = 384;
-constexpr int kManyRows = 128;                        // rows of a CTA; the pair has twice as many
+constexpr int kManyRows = 128;                        // rows of a CTA
 constexpr int kManyFeatures = 256;
-constexpr int kManyABytes = kManyRows * BK;
-constexpr int kManyWBytes = kManyFeatures / 2 * BK;   // this CTA's weight rows
-constexpr int kManyStageBytes = kManyABytes + kManyWBytes;
-constexpr int kManyStages = 6;
 constexpr int kManyDrain = 8;                         // drain warps
 constexpr int kManyEpiBuf = 32 * 64;                  // per drain warp: 32 rows x 64 bytes
-constexpr int kManySmem = kManyStages * kManyStageBytes + kManyDrain * kManyEpiBuf + 1024;
+template <bool PAIR>
+struct ManyCfg {
+    static constexpr int kRows = PAIR ? 2 * kManyRows : kManyRows;               // of a tile
+    static constexpr int kWRows = PAIR ? kManyFeatures / 2 : kManyFeatures;      // weight rows in a CTA
+    static constexpr int kABytes = kManyRows * BK;
+    static constexpr int kStageBytes = kABytes + kWRows * BK;
+    static constexpr int kStages = PAIR ? 6 : 4;
+    static constexpr int kSmem = kStages * kStageBytes + kManyDrain * kManyEpiBuf + 1024;
+};
 
 // 4-byte asynchronous copy, counted by cp.async.mbarrier.arrive.
 __device__ __forceinline__ void cp_async_4(float* dst, const float* src) {
@@ -473,15 +506,6 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
         "%4}], [%2];" ::"r"(ptx::smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(x), "r"(y)
-        : "memory");
-}
-__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                               uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 // Arrive on a barrier of the pair (a shared::cluster address). What it orders are TMEM reads, which the
@@ -498,10 +522,27 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
         "h"((uint16_t)3)
         : "memory");
 }
+// The same on this CTA's barrier alone.
+__device__ __forceinline__ void umma_commit_leader(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(ptx::smem_u32(bar))
+                 : "memory");
+}
+// One warp of each CTA of the pair.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_u32(dst_smem)),
+                 "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kManyThreads, 1)
+template <bool PAIR>   // launched in clusters of two
+__global__ void __launch_bounds__(kManyThreads, 1)
 k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w, Problem p) {
-    constexpr int S = kManyStages;
+    using C = ManyCfg<PAIR>;
+    constexpr int S = C::kStages;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S], acc_full[2], acc_empty[2], sc_full[2], sc_empty[2],
         mma_done;
@@ -514,15 +555,16 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)ptx::cluster_ctarank(), pair = (int)ptx::cluster_id_x(), pairs = (int)ptx::nclusters_x();
+    const int rank = PAIR ? (int)ptx::cluster_ctarank() : 0;
+    const int t0 = PAIR ? (int)ptx::cluster_id_x() : blockIdx.x, t_step = PAIR ? (int)ptx::nclusters_x() : gridDim.x;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            ptx::mbar_init(&full_bar[i], 1);     // the leader's: its producer, and both CTAs' bytes
-            ptx::mbar_init(&empty_bar[i], 1);    // the leader's commit
+            ptx::mbar_init(&full_bar[i], 1);     // of a pair the leader's: its producer, and both CTAs' bytes
+            ptx::mbar_init(&empty_bar[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&acc_full[i], 1);
-            ptx::mbar_init(&acc_empty[i], 2 * kManyDrain);   // the leader's: the drain warps of both CTAs
+            ptx::mbar_init(&acc_empty[i], (PAIR ? 2 : 1) * kManyDrain);   // of a pair the leader's
             ptx::mbar_init(&sc_full[i], 32);
             ptx::mbar_init(&sc_empty[i], kManyDrain);
         }
@@ -533,20 +575,22 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
         ptx::tma_prefetch_desc(&tma_w);
     }
     if (warp == 3) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_u32(&tmem_slot)),
-                     "r"(512)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        if (PAIR) {
+            tmem_alloc_pair(&tmem_slot, 512);
+        } else {
+            ptx::tmem_alloc(&tmem_slot, 512);
+            ptx::tmem_relinquish();
+        }
     }
     griddep_wait();
-    build_groups(G, p, 2 * kManyRows, (p.n + kManyFeatures - 1) / kManyFeatures);
+    build_groups(G, p, C::kRows, (p.n + kManyFeatures - 1) / kManyFeatures);
     ptx::tc_fence_before();
     __syncthreads();
-    ptx::cluster_sync_all();   // the peer's barriers are set up before anything arrives on them
+    if (PAIR) ptx::cluster_sync_all();   // the peer's barriers are set up before anything arrives on them
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const int tiles = G.start[p.groups];
-    // Features of a tile, a multiple of 16: the UMMA's N. The first half are the leader's weight rows.
+    // Features of a tile, a multiple of 16: the UMMA's N. Of a pair's, the first half are the leader's weight rows.
     auto width_of = [&](int f0) { return min(kManyFeatures, p.n - f0); };
 
     if (warp < 4) {
@@ -556,24 +600,30 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
             // ---------------- TMA: this CTA's rows of x and of the weight tile
             int stage = 0, issued = 0;
             uint32_t phase = 0;
-            for (int t = pair; t < tiles; t += pairs) {
-                const Tile tl = tile_at(G, p.groups, t, 2 * kManyRows, kManyFeatures);
+            for (int t = t0; t < tiles; t += t_step) {
+                const Tile tl = tile_at(G, p.groups, t, C::kRows, kManyFeatures);
                 const int x_row = tl.row0 + rank * kManyRows;
-                const int w_row = tl.g * p.n + tl.f0 + rank * (width_of(tl.f0) / 2);
+                const int w_row = tl.g * p.n + tl.f0 + (PAIR ? rank * (width_of(tl.f0) / 2) : 0);
                 for (int kb = 0; kb < p.kb; ++kb) {
                     if (!ptx::mbar_wait(&empty_bar[stage], phase ^ 1, p.status)) { abort_flag = 1; goto loads_done; }
                     if (*(volatile int*)&abort_flag) goto loads_done;
-                    unsigned char* x_s = smem + stage * kManyStageBytes;
-                    const uint32_t bar = ptx::mapa_shared(ptx::smem_u32(&full_bar[stage]), 0);
-                    if (rank == 0) ptx::mbar_arrive_expect_tx(&full_bar[stage], 2 * kManyStageBytes);
-                    tma_load_2d_pair(x_s, &tma_x, bar, kb * BK, x_row);
-                    tma_load_2d_pair(x_s + kManyABytes, &tma_w, bar, kb * BK, w_row);
+                    unsigned char* x_s = smem + stage * C::kStageBytes;
+                    if (PAIR) {
+                        const uint32_t bar = ptx::mapa_shared(ptx::smem_u32(&full_bar[stage]), 0);
+                        if (rank == 0) ptx::mbar_arrive_expect_tx(&full_bar[stage], 2 * C::kStageBytes);
+                        tma_load_2d_pair(x_s, &tma_x, bar, kb * BK, x_row);
+                        tma_load_2d_pair(x_s + C::kABytes, &tma_w, bar, kb * BK, w_row);
+                    } else {
+                        ptx::mbar_arrive_expect_tx(&full_bar[stage], C::kStageBytes);
+                        ptx::tma_load_2d(x_s, &tma_x, &full_bar[stage], kb * BK, x_row);
+                        ptx::tma_load_2d(x_s + C::kABytes, &tma_w, &full_bar[stage], kb * BK, w_row);
+                    }
                     ++issued;
                     if (++stage == S) { stage = 0; phase ^= 1; }
                 }
             }
         loads_done:
-            if (rank == 0)   // both CTAs' loads land before shared memory is released (the pair leaves together)
+            if (rank == 0)   // every load lands before shared memory is released (a pair leaves together)
                 for (int i = 0; i < S && i < issued; ++i) {
                     if (--stage < 0) { stage = S - 1; phase ^= 1; }
                     ptx::mbar_wait(&full_bar[stage], phase, p.status);
@@ -581,39 +631,23 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
         } else if ((warp == 1 || warp == 2) && lane == 0 && rank == 0) {
             // ---------------- UMMA: every second K block each
             const int q = warp - 1;
-            int stage = q;
-            uint32_t phase = 0, acc_phase = 0;
-            long long next = q, before = 0;   // blocks, over all tiles of the pair
-            bool ok = true;
-            for (int t = pair; ok && t < tiles; t += pairs) {
-                const uint32_t idesc =
-                    idesc_e4m3(2 * kManyRows, width_of(tile_at(G, p.groups, t, 2 * kManyRows, kManyFeatures).f0));
-                for (; next < before + p.kb; next += 2) {
-                    if (!ptx::mbar_wait(&full_bar[stage], phase, p.status) ||
-                        !ptx::mbar_wait(&acc_empty[q], acc_phase ^ 1, p.status)) {
-                        abort_flag = 1;
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after();
-                    const uint32_t x_addr = ptx::smem_u32(smem + stage * kManyStageBytes);
+            const bool ok = issue_blocks<S, 2>(
+                q, my_tiles(tiles, t0, t_step), p.kb, full_bar, empty_bar, acc_full, acc_empty, p.status,
+                [&](int i) {
+                    const Tile tl = tile_at(G, p.groups, t0 + i * t_step, C::kRows, kManyFeatures);
+                    return idesc_e4m3(C::kRows, width_of(tl.f0));
+                },
+                [&](uint32_t idesc, int stage, int buf) {
+                    const uint32_t x_addr = ptx::smem_u32(smem + stage * C::kStageBytes);
                     const uint64_t xd = ptx::sdesc_sw128(x_addr, 16, 1024);
-                    const uint64_t wd = ptx::sdesc_sw128(x_addr + kManyABytes, 16, 1024);
-                    // past K both operands are zero-filled, so a partial last block has no other form
+                    const uint64_t wd = ptx::sdesc_sw128(x_addr + C::kABytes, 16, 1024);
 #pragma unroll
-                    for (int kk = 0; kk < BK / 32; ++kk)   // K = 32 further: 32 bytes, 2 in the descriptor's units
-                        umma_e4m3_pair(tmem + q * kManyFeatures, xd + 2 * kk, wd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
-                    umma_commit_pair(&acc_full[q]);
-                    umma_commit_pair(&empty_bar[stage]);
-                    acc_phase ^= 1;
-                    stage += 2;
-                    if (stage >= S) { stage -= S; phase ^= 1; }
-                }
-                before += p.kb;
-            }
-            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                             ptx::smem_u32(&mma_done))
-                         : "memory");   // all UMMAs complete before TMEM is released
+                    for (int kk = 0; kk < BK / 32; ++kk)
+                        umma_e4m3<PAIR>(tmem + buf * kManyFeatures, xd + 2 * kk, wd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+                },
+                [](uint64_t* bar) { PAIR ? umma_commit_pair(bar) : ptx::umma_commit(bar); });
+            if (!ok) abort_flag = 1;
+            PAIR ? umma_commit_leader(&mma_done) : ptx::umma_commit(&mma_done);   // all UMMAs complete before TMEM is released
             ptx::mbar_wait(&mma_done, 0, p.status);
         } else if (warp == 3) {
             // ---------------- scales: 128 row scales and two weight scales a block, kScales blocks
@@ -622,8 +656,8 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
             int slot = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int t = pair; ok && t < tiles; t += pairs) {
-                const Tile tl = tile_at(G, p.groups, t, 2 * kManyRows, kManyFeatures);
+            for (int t = t0; ok && t < tiles; t += t_step) {
+                const Tile tl = tile_at(G, p.groups, t, C::kRows, kManyFeatures);
                 const int r0 = tl.row0 + rank * kManyRows + lane;
                 const float* ws = p.ws + ((size_t)tl.g * p.nb + min((tl.f0 >> 7) + (lane & 1), p.nb - 1)) * p.kb + (lane >> 1);
                 for (int k0 = 0; k0 < p.kb; k0 += kScales) {
@@ -647,13 +681,13 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
         // ---------------- drain: thread = row of TMEM lane quarter warp & 3, columns [128 cg, 128 cg + 128)
         const int quarter = warp & 3, cg = (warp - 4) >> 2;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + 128 * cg;
-        const uint32_t freed = ptx::mapa_shared(ptx::smem_u32(&acc_empty[0]), 0);   // the leader's
+        const uint32_t freed = PAIR ? ptx::mapa_shared(ptx::smem_u32(&acc_empty[0]), 0) : 0;   // the leader's
         const float* my_x = &x_sc[0][0][quarter * 32 + lane];
         const float* my_w = &w_sc[0][0][cg];
         int slot = 0, q = 0;
         uint32_t sc_phase = 0, acc_phase = 0;
         bool ok = true;
-        for (int t = pair; ok && t < tiles; t += pairs) {
+        for (int t = t0; ok && t < tiles; t += t_step) {
             float acc[4][32];
             uint32_t d[2][32];
 #pragma unroll
@@ -706,7 +740,7 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
                 ptx::tmem_wait_ld32(d[1]);
                 ptx::tc_fence_before();   // all in registers: the accumulator is free
                 __syncwarp();
-                if (lane == 0) arrive_cluster(freed + 8 * q);
+                if (lane == 0) PAIR ? arrive_cluster(freed + 8 * q) : ptx::mbar_arrive(&acc_empty[q]);
                 q ^= 1;
                 if (q == 0) acc_phase ^= 1;
             }
@@ -715,8 +749,8 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
                 break;
             }
             add(acc[3], d[1], s);
-            const Tile tl = tile_at(G, p.groups, t, 2 * kManyRows, kManyFeatures);
-            unsigned char* ebuf = smem + S * kManyStageBytes + (warp - 4) * kManyEpiBuf;
+            const Tile tl = tile_at(G, p.groups, t, C::kRows, kManyFeatures);
+            unsigned char* ebuf = smem + S * C::kStageBytes + (warp - 4) * kManyEpiBuf;
             const int f = tl.f0 + 128 * cg, row0 = rank * kManyRows + quarter * 32;
             // Out through shared memory, 64 bytes a row at a time (32 16-bit or 16 fp32 columns):
             // 16-byte pieces, swizzled by the row so that neither side has bank conflicts; four
@@ -775,10 +809,10 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
     }
     ptx::tc_fence_before();
     __syncthreads();
-    ptx::cluster_sync_all();   // no UMMA reads the peer's memory, no arrival is under way any more
+    if (PAIR) ptx::cluster_sync_all();   // no UMMA reads the peer's memory, no arrival is under way any more
     if (warp == 3) {
         ptx::tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+        PAIR ? tmem_dealloc_pair(tmem, 512) : ptx::tmem_dealloc(tmem, 512);
     }
 }
 

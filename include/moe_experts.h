@@ -86,7 +86,8 @@ int mla_moe_sort(const int32_t* topk_idx, const void* affinities, int n_tokens, 
  *   rows    [n_rows, hidden] of `dtype` when scales is NULL; else e4m3, with
  *   scales  [ceil(hidden / 128), n_rows] fp32 (quantised as mla_fp8_quantize does)
  *
- * Limits: hidden a positive multiple of 16; 1 <= top_k <= 32; n_tokens, n_rows >= 0. */
+ * Limits: hidden a positive multiple of 16, up to 2^30; 1 <= top_k <= 32; n_tokens and
+ * n_rows >= 0, n_tokens * top_k <= 2^30, n_tokens * hidden < 2^42. */
 int mla_moe_gather(const void* x, int dtype, const int32_t* row_of, int n_tokens, int top_k, int hidden, int n_rows,
                    void* rows, float* scales, void* stream);
 
@@ -138,7 +139,8 @@ int mla_fp8_quantize(const void* x, int dtype, int n_rows, int cols, int gated, 
  *             on-device wait gave up (the output is invalid then); never cleared by the call
  *             (read it with mla_get_device_status)
  *
- * Limits: n and k positive multiples of 16, n_rows >= 0. */
+ * Limits: n and k positive multiples of 16, up to 2^30; n_rows from 0 to 2^30, and n_rows * n
+ * < 2^40. */
 int mla_fp8_matmul(const void* x, const float* x_scales, const void* w, const float* w_scales, int n_rows, int n,
                    int k, void* out, int out_dtype, int32_t* status, void* stream);
 

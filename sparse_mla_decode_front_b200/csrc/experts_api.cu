@@ -42,7 +42,7 @@ bool sort_dims_ok(int T, int K, int E) {
 int row_dims(int T, int K, int H, int R, int dtype) {
     if (T < 0 || K < 1 || H < 1 || R < 0) return MLA_ERR_BAD_DIMS;
     if (!dtype_ok(dtype)) return MLA_ERR_BAD_ARGUMENT;
-    if (K > MLA_MOE_MAX_TOP_K || H % 16 || (long long)T * K > (1LL << 30) || !moe_rows_fit(T, H))
+    if (K > MLA_MOE_MAX_TOP_K || H % 16 || H > (1 << 30) || (long long)T * K > (1LL << 30) || !moe_rows_fit(T, H))
         return MLA_ERR_UNSUPPORTED_DIMS;
     return MLA_OK;
 }

@@ -2,6 +2,7 @@
 #include "fp8_gemm.cuh"
 
 #include <algorithm>
+#include <mutex>
 
 namespace mla {
 namespace {
@@ -47,7 +48,9 @@ int few_split(long long tiles, int kb, const int (&clusters)[4]) {
     return 1 << i;
 }
 
-// What the host knows of one width of k_fp8_few on a device: resident clusters of 1, 2, 4 and 8 CTAs.
+// What the host knows of one width of k_fp8_few on a device: resident clusters of 1, 2, 4 and 8
+// CTAs. Host threads that call for the first time at once see the same values (the split decides
+// the order of the sums).
 struct FewDevice {
     int clusters[4];
     bool known;
@@ -55,8 +58,10 @@ struct FewDevice {
 
 template <int BN>
 cudaError_t few_device(int dev, FewDevice* out) {
+    static std::mutex mu;
     static FewDevice cached[kMaxDevices] = {};
     const bool keep = dev >= 0 && dev < kMaxDevices;
+    std::lock_guard<std::mutex> lock(mu);
     if (keep && cached[dev].known) {
         *out = cached[dev];
         return cudaSuccess;
@@ -175,9 +180,10 @@ cudaError_t choose(const fp8::Problem& p, int dev, int* width) {
 
 }  // namespace
 
-// Tiles are counted in 32 bits (the smallest row tile is 16).
+// Rows, and tiles (the smallest row tile is 16) plus a step of the grid, are counted in 32 bits.
 bool fp8_gemm_fits(int rows, int groups, int n) {
-    return ((long long)rows / 16 + groups) * ((n + 127) / 128) < (1LL << 31) && (long long)groups * n < (1LL << 31);
+    return rows <= (1 << 30) && ((long long)rows / 16 + groups) * ((n + 127) / 128) < (1LL << 30) &&
+           (long long)groups * n < (1LL << 31);
 }
 
 cudaError_t launch_fp8_gemm(const void* x, const float* xs, const void* w, const float* ws, const int32_t* offsets,

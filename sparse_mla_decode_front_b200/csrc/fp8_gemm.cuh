@@ -538,7 +538,7 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-template <bool PAIR>   // launched in clusters of two
+template <bool PAIR>   // PAIR: launched in clusters of two
 __global__ void __launch_bounds__(kManyThreads, 1)
 k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w, Problem p) {
     using C = ManyCfg<PAIR>;

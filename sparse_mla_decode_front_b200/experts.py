@@ -130,7 +130,7 @@ def mla_moe_sort(topk_idx, expert_offsets, row_of, source_of, workspace=None, fi
         ws_bytes = _shape("workspace", workspace, 1)[0]
         ws = _ptr("workspace", workspace, torch.uint8, (ws_bytes,), dev)
     _call("mla_moe_sort", _lib_of().mla_moe_sort, dev, stream, _ptr("topk_idx", topk_idx, i32, tk, dev), aff, T, K, total,
-          first_expert, E, 1 if normalize else 0, scale,
+          int(first_expert), E, 1 if normalize else 0, float(scale),
           _ptr("expert_offsets", expert_offsets, i32, (E + 1,), dev), _ptr("row_of", row_of, i32, tk, dev),
           _ptr("source_of", source_of, i32, (T * K,), dev), w, ws, ws_bytes)
 
@@ -176,7 +176,8 @@ def mla_moe_combine_backward(grad_out, rows, row_of, weights: Optional[torch.Ten
     K, R = _shape("row_of", row_of, 2)[1], _shape("rows" if rows is not None else "grad_rows", held, 2)[0]
     opt = lambda name, t, dtype, shape: None if t is None else _ptr(name, t, dtype, shape, dev)
     _call("mla_moe_combine_backward", _lib_of().mla_moe_combine_backward, dev, stream,
-          _ptr("grad_out", grad_out, grad_out.dtype, th, dev), opt("rows", rows, grad_out.dtype, (R, H)), code, _ptr("row_of", row_of, torch.int32, (T, K), dev),
+          _ptr("grad_out", grad_out, grad_out.dtype, th, dev), opt("rows", rows, grad_out.dtype, (R, H)), code,
+          _ptr("row_of", row_of, torch.int32, (T, K), dev),
           opt("weights", weights, torch.float32, (T, K)), T, K, H, R,
           opt("grad_rows", grad_rows, grad_out.dtype, (R, H)), opt("grad_weights", grad_weights, torch.float32, (T, K)))
 

@@ -193,7 +193,8 @@ def test_quantize_special_values():
     x[5] = torch.tensor([448.0, -448.0], device="cuda").repeat(128)
     q, scales = filled(6, 256, dtype=E4M3), filled(2, 6, dtype=torch.float32)
     G.mla_fp8_quantize(x, q, scales)
-    back = f64(q.float()) * np.repeat(f64(scales).T, 128, 1)
+    with np.errstate(invalid="ignore"):                # 0 times an infinite scale
+        back = f64(q.float()) * np.repeat(f64(scales).T, 128, 1)
     assert not back[0].any() and np.isfinite(f64(scales)[:, 0]).all()
     assert np.isnan(back[1, :128]).all() and not back[1, 128:].any()
     assert np.isnan(back[2, 128:]).all() and not back[2, :128].any()
@@ -320,6 +321,61 @@ def test_matmul(M, N, K, dtype):
     torch.cuda.synchronize()
     assert api.mla_get_device_status(status) == 0
     check_product(out, x, xs, w[0], ws[0], dtype)
+
+
+# every width of a feature tile, several tiles a CTA (pair) with an odd count of K blocks, and K
+# split over clusters of 2, 4 and 8 CTAs with runs of unequal length
+WIDE = [(300, n, 256) for n in range(16, 257, 16)] + [(4100, 1040, 272), (33, 20480, 272), (150, 9600, 400)]
+SPLIT = [(m, n, k) for m, n in [(1, 16), (20, 144), (64, 272), (100, 2048)] for k in (512, 640, 1168, 2064, 4112)]
+
+
+@pytest.mark.parametrize("M,N,K", WIDE + SPLIT)
+def test_matmul_tilings(M, N, K):
+    x, xs = make_operand(M, K, M + N)
+    w, ws = make_weight(1, N, K, N + K)
+    buf = filled(M + 2, N, dtype=torch.bfloat16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    G.mla_fp8_matmul(x, xs, w[0], ws[0], buf[1:M + 1], status)
+    torch.cuda.synchronize()
+    assert int(status) == 0 and untouched(buf[0]) and untouched(buf[-1])
+    check_product(buf[1:M + 1], x, xs, w[0], ws[0], torch.bfloat16)
+
+
+@pytest.mark.parametrize("N,K", [(n, 272) for n in range(16, 257, 48)] + [(1040, 272)])
+def test_grouped_matmul_tilings(N, K):
+    counts = [300] * 6 + [1, 127, 128, 129, 515]       # 1040: more tiles than CTAs
+    off = np.concatenate([[0], np.cumsum(counts)])
+    x, xs = make_operand(int(off[-1]), K, N)
+    w, ws = make_weight(len(counts), N, K, K)
+    out = filled(int(off[-1]), N, dtype=torch.bfloat16)
+    G.mla_fp8_grouped_matmul(x, xs, w, ws, torch.tensor(off, dtype=torch.int32, device="cuda"), out)
+    for e, c in enumerate(counts):
+        part = slice(off[e], off[e + 1])
+        check_product(out[part], x[part], xs[:, part], w[e], ws[e], torch.bfloat16, f"expert {e}")
+
+
+def test_offsets_beyond_32_bits():
+    # an output of 2.3e9 elements, rows gathered into 2.4e9 bytes, and back
+    M, N, K = 70001, 32768, 128
+    x, xs = make_operand(M, K, 1)
+    w, ws = make_weight(1, N, K, 2)
+    out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    G.mla_fp8_matmul(x, xs, w[0], ws[0], out)
+    at = [0, 65535, 65536, M - 1]
+    check_product(out[at], x[at], xs[:, at].contiguous(), w[0], ws[0], torch.bfloat16)
+    del out
+    T, H, R = 50, 8192, 300007
+    v = torch.randn(T, H, generator=gen(3), device="cuda").to(torch.bfloat16)
+    row_of = (R - 1 - 6000 * torch.arange(T, device="cuda", dtype=torch.int32)).reshape(T, 1)
+    rows, scales = torch.zeros(R, H, dtype=torch.uint8, device="cuda").view(E4M3), torch.zeros(64, R, device="cuda")
+    G.mla_moe_gather(v, row_of, rows, scales)
+    r = row_of[:, 0].long()
+    check_quantized(rows[r].float(), scales[:, r], f64(v), 0.0)
+    wide = torch.zeros(R, H, dtype=torch.bfloat16, device="cuda")
+    G.mla_moe_gather(v, row_of, wide)
+    back = torch.empty_like(v)
+    G.mla_moe_combine(wide, row_of, None, back)
+    assert torch.equal(back, v)
 
 
 GROUPS = {
@@ -520,6 +576,53 @@ def test_layer_in_a_graph_and_on_another_stream():
         torch.cuda.synchronize()
         assert torch.equal(layer.out, replayed)        # the same from run to run
     assert not torch.equal(first, layer.out)
+
+
+def test_chunked_sort_and_products_in_a_graph():
+    layer = Layer(1201, 512, 128, 64, 8, 0, 64, seed=71)   # 9608 choices: two launches, a workspace
+    layer.run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=s):
+        layer.run(s)
+    for seed in (72, 73):
+        layer.x.copy_(torch.randn(layer.T, layer.H, generator=gen(seed), device="cuda"))
+        torch.cuda.synchronize()
+        g.replay()
+        g.replay()
+        layer.check()
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    code = """
+import torch
+from sparse_mla_decode_front_b200 import experts as G
+idx = torch.randint(0, 64, (600, 8), device="cuda", dtype=torch.int32)
+off, row, src = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (65, 4800, 4800))
+ws = torch.empty(G.mla_moe_sort_workspace_bytes(600, 8, 64), dtype=torch.uint8, device="cuda")
+x = torch.ones(3, 512, device="cuda").to(torch.float8_e4m3fn)
+w = torch.ones(64, 512, device="cuda").to(torch.float8_e4m3fn)
+xs, wsc, out = torch.ones(4, 3, device="cuda"), torch.ones(1, 4, device="cuda"), torch.zeros(3, 64, device="cuda")
+big, bs = torch.ones(600, 512, device="cuda").to(torch.float8_e4m3fn), torch.ones(4, 600, device="cuda")
+bout = torch.zeros(600, 64, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    G.mla_moe_sort(idx, off, row.view(600, 8), src, ws)
+    G.mla_fp8_matmul(x, xs, w, wsc, out)
+    G.mla_fp8_matmul(big, bs, w, wsc, bout)
+g.replay()
+torch.cuda.synchronize()
+assert int(off[-1]) == 4800 and bool((out == 512).all()) and bool((bout == 512).all())
+print("fine")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
 
 
 def test_two_layers_on_two_streams_at_once():

@@ -5,7 +5,9 @@ tensors as-is, the paged cache as a zero-filled pool into which the filled
 rows are scattered. ``DecodeStep`` keeps them resident with the output and
 workspace buffers and runs the C-ABI call, either from device-resident inputs
 or from pinned host copies of the per-step inputs (hidden states, RoPE tables
-and index tensors), reading the output back to the host.
+and index tensors), reading the output back to the host. ``ExpertLayer`` does
+the same for the MoE layer that follows the block: the router and the routed
+experts this rank holds.
 """
 from __future__ import annotations
 
@@ -14,7 +16,7 @@ from typing import Dict, Optional
 import numpy as np
 import torch
 
-from . import api
+from . import api, experts
 
 PER_STEP_INPUTS = ("hidden_states", "cos", "sin", "slot_mapping", "block_table", "positions",
                    "gather_indices")
@@ -186,3 +188,61 @@ class DecodeStep:
         comp.wait_stream(down)
         self.pipe_last_out = host_out[(n_steps - 1) % 2]   # the last step's output, on the host
         return start.elapsed_time(end)
+
+
+class ExpertLayer:
+    """Resident weights and buffers of a MoE layer's routed experts, for ``n_tokens`` tokens a
+    step: fused RMSNorm + router top-K, the choices sorted by expert, the rows gathered as e4m3,
+    the gate | up product, the gated activation, the down product and the weighted sum back.
+
+    The experts of this rank are ``w_up`` [E, 2 * width, hidden] and ``w_down`` [E, hidden, width]
+    (e4m3, scales [E, ceil(n / 128), ceil(k / 128)]), global ids from ``first_expert`` on;
+    ``router_weights`` [hidden, all experts]. Choices of other ranks' experts are left out: the
+    outputs of all ranks add up to the layer's. ``run`` allocates nothing and can be captured."""
+
+    def __init__(self, n_tokens: int, gamma, router_weights, w_up, w_up_scales, w_down, w_down_scales, top_k: int,
+                 first_expert: int = 0, router_bias=None, act: str = "sigmoid", normalize: bool = True,
+                 scale: float = 1.0, eps: float = 1e-6):
+        self.gamma, self.router_weights, self.router_bias = gamma, router_weights, router_bias
+        self.w_up, self.w_up_scales, self.w_down, self.w_down_scales = w_up, w_up_scales, w_down, w_down_scales
+        self.top_k, self.first_expert, self.act = top_k, first_expert, act
+        self.normalize, self.scale, self.eps = normalize, scale, eps
+        T, K, (held, hidden, width), n_experts = n_tokens, top_k, w_down.shape, router_weights.shape[1]
+        rows, dev = T * K, w_down.device
+        new = lambda *shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
+        nbytes = api.mla_router_workspace_bytes(T, hidden, n_experts, K)
+        if nbytes == 0:
+            raise api.MlaError(api._lib.MLA_ERR_UNSUPPORTED_DIMS, "mla_router_workspace_bytes")
+        self.router_workspace = new(nbytes, dtype=torch.uint8)
+        nbytes = experts.mla_moe_sort_workspace_bytes(T, K, held)
+        self.sort_workspace = new(nbytes, dtype=torch.uint8) if nbytes else None
+        bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+        self.norm, self.affinities = new(T, hidden, dtype=bf16), new(T, n_experts, dtype=bf16)
+        self.topk_idx, self.row_of = new(T, K, dtype=i32), new(T, K, dtype=i32)
+        self.expert_offsets, self.source_of = new(held + 1, dtype=i32), new(rows, dtype=i32)
+        self.weights = new(T, K, dtype=f32)
+        self.x, self.x_scales = new(rows, hidden, dtype=experts.E4M3), new(experts.scale_blocks(hidden), rows, dtype=f32)
+        self.gate_up = new(rows, 2 * width, dtype=bf16)
+        self.h, self.h_scales = new(rows, width, dtype=experts.E4M3), new(experts.scale_blocks(width), rows, dtype=f32)
+        self.y, self.out = new(rows, hidden, dtype=bf16), new(T, hidden, dtype=bf16)
+        self.status = torch.zeros(1, dtype=i32, device=dev)
+
+    def run(self, hidden_states: torch.Tensor, stream=None) -> torch.Tensor:
+        """``out`` [n_tokens, hidden] of ``hidden_states`` (bf16), enqueued on ``stream``."""
+        api.mla_rmsnorm_router_topk(hidden_states, self.gamma, self.router_weights, self.router_bias, self.eps,
+                                    self.top_k, self.act, self.norm, self.topk_idx, self.affinities,
+                                    self.router_workspace, stream)
+        experts.mla_moe_sort(self.topk_idx, self.expert_offsets, self.row_of, self.source_of, self.sort_workspace,
+                             self.first_expert, self.affinities, self.weights, self.normalize, self.scale, stream)
+        experts.mla_moe_gather(self.norm, self.row_of, self.x, self.x_scales, stream)
+        experts.mla_fp8_grouped_matmul(self.x, self.x_scales, self.w_up, self.w_up_scales, self.expert_offsets,
+                                       self.gate_up, self.status, stream)
+        experts.mla_fp8_quantize(self.gate_up, self.h, self.h_scales, True, self.expert_offsets[-1:], stream)
+        experts.mla_fp8_grouped_matmul(self.h, self.h_scales, self.w_down, self.w_down_scales, self.expert_offsets,
+                                       self.y, self.status, stream)
+        experts.mla_moe_combine(self.y, self.row_of, self.weights, self.out, stream)
+        return self.out
+
+    def device_status(self, stream=None) -> int:
+        """Bits of the waits that gave up since the layer was made (0: none)."""
+        return api.mla_get_device_status(self.status, stream)

@@ -19,6 +19,7 @@ import torch
 
 from oracle import moe_experts as X
 from sparse_mla_decode_front_b200 import _lib, api, experts as G
+from sparse_mla_decode_front_b200.device import ExpertLayer
 
 pytestmark = pytest.mark.gpu
 
@@ -472,51 +473,37 @@ def test_nan_stays_in_its_row_and_column():
 
 # ------------------------------------------------------------------ together
 class Layer:
-    """The router and its experts, as a decode step or a prompt chunk runs them."""
+    """The router and its experts, as a decode step or a prompt chunk runs them (device.ExpertLayer),
+    with every buffer filled with a sentinel first."""
 
     def __init__(self, T, H, I, E, K, first, held, seed):
         g = gen(seed)
         rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
         self.T, self.H, self.I, self.E, self.K, self.first, self.held = T, H, I, E, K, first, held
         self.x = rnd(T, H).to(torch.bfloat16)
-        self.gamma = (1 + 0.1 * rnd(H)).to(torch.bfloat16)
-        self.router_w = (rnd(H, E) / H ** 0.5).to(torch.bfloat16)
+        gamma = (1 + 0.1 * rnd(H)).to(torch.bfloat16)
+        router_w = (rnd(H, E) / H ** 0.5).to(torch.bfloat16)
         self.w1, self.s1 = make_weight(held, 2 * I, H, seed + 1)
         self.w2, self.s2 = make_weight(held, H, I, seed + 2)
         self.s1 *= 2.0 ** -3 * (512 / H) ** 0.5
-        R = T * K
-        new = lambda *s, dtype: filled(*s, dtype=dtype)
-        self.norm, self.idx = new(T, H, dtype=torch.bfloat16), new(T, K, dtype=torch.int32)
-        self.aff = new(T, E, dtype=torch.bfloat16)
-        self.rws = new(api.mla_router_workspace_bytes(T, H, E, K), dtype=torch.uint8)
-        self.off, self.row, self.src = (new(held + 1, dtype=torch.int32), new(T, K, dtype=torch.int32),
-                                        new(R, dtype=torch.int32))
-        self.wt = new(T, K, dtype=torch.float32)
-        n = G.mla_moe_sort_workspace_bytes(T, K, held)
-        self.sws = new(n, dtype=torch.uint8) if n else None
-        self.q, self.qs = new(R, H, dtype=E4M3), new(G.scale_blocks(H), R, dtype=torch.float32)
-        self.h, self.a = new(R, 2 * I, dtype=torch.bfloat16), new(R, I, dtype=E4M3)
-        self.as_ = new(G.scale_blocks(I), R, dtype=torch.float32)
-        self.y, self.out = new(R, H, dtype=torch.bfloat16), new(T, H, dtype=torch.bfloat16)
-        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.layer = layer = ExpertLayer(T, gamma, router_w, self.w1, self.s1, self.w2, self.s2, K, first, scale=2.5)
+        for name in ("norm", "affinities", "topk_idx", "row_of", "expert_offsets", "source_of", "weights", "x",
+                     "x_scales", "gate_up", "h", "h_scales", "y", "out", "router_workspace", "sort_workspace"):
+            t = getattr(layer, name)
+            if t is not None:
+                t.view(torch.uint8).fill_(SENTINEL)
+        self.norm, self.idx, self.aff = layer.norm, layer.topk_idx, layer.affinities
+        self.off, self.row, self.wt, self.out, self.status = (layer.expert_offsets, layer.row_of, layer.weights,
+                                                              layer.out, layer.status)
 
     def run(self, stream=None):
-        api.mla_rmsnorm_router_topk(self.x, self.gamma, self.router_w, None, 1e-6, self.K, "sigmoid", self.norm,
-                                    self.idx, self.aff, self.rws, stream)
-        G.mla_moe_sort(self.idx, self.off, self.row, self.src, self.sws, self.first, self.aff, self.wt, True, 2.5,
-                       stream)
-        G.mla_moe_gather(self.norm, self.row, self.q, self.qs, stream)
-        G.mla_fp8_grouped_matmul(self.q, self.qs, self.w1, self.s1, self.off, self.h, self.status, stream)
-        G.mla_fp8_quantize(self.h, self.a, self.as_, True, self.off[self.held:], stream)
-        G.mla_fp8_grouped_matmul(self.a, self.as_, self.w2, self.s2, self.off, self.y, self.status, stream)
-        G.mla_moe_combine(self.y, self.row, self.wt, self.out, stream)
-        return self.out
+        return self.layer.run(self.x, stream)
 
     def check(self):
         """The layer's output against the oracle on the layer's own norm rows and choices, with the
         8-bit roundings of the path (2^-4 an element, averaging out over a product) bounded in norm."""
         torch.cuda.synchronize()
-        assert int(self.status) == 0
+        assert self.layer.device_status() == 0
         idx, x = self.idx.cpu().numpy(), f64(self.norm)
         s = X.sort(idx, self.first, self.held)
         assert np.array_equal(self.off.cpu().numpy(), s["expert_offsets"])

@@ -3,7 +3,9 @@
     python -m sparse_mla_decode_front_b200.build
 
 compiles every ``csrc/*.cu`` into ``libsparse_mla_decode.so`` next to this
-file (cudart linked statically). Rebuilds only when a source is newer.
+file (cudart linked statically), and ``csrc/bind.cpp`` (g++, against torch's
+headers) into ``_bind.so``, the experts binding's native argument checks.
+Rebuilds only when a source is newer.
 """
 from __future__ import annotations
 
@@ -12,10 +14,12 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libsparse_mla_decode.so")
+BIND = os.path.join(HERE, "_bind.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -42,7 +46,31 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in deps())
 
 
+def build_bind(force: bool = False, verbose: bool = False) -> str:
+    """``_bind.so``: it calls the library through addresses it is given, and links torch only."""
+    src = os.path.join(HERE, "csrc", "bind.cpp")
+    used = [src, os.path.join(ROOT, "include", "moe_experts.h")]
+    if not force and os.path.exists(BIND) and all(os.path.getmtime(f) <= os.path.getmtime(BIND) for f in used):
+        return BIND
+    import torch
+    site = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    include = [sysconfig.get_paths()["include"], os.path.join(site, "include"),
+               os.path.join(site, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    tmp = BIND + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+           *[a for d in include for a in ("-isystem", d)], src, "-o", tmp, "-L" + os.path.join(site, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    build_bind(force, verbose)
     if not force and up_to_date():
         return LIB
     out_dir = os.path.join(HERE, "_build")

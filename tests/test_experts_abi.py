@@ -113,3 +113,19 @@ def test_binding_refuses_host_tensors_and_missing_arguments():
             call()
     with pytest.raises(ValueError, match="None"):
         experts.mla_moe_gather(None, t, t)
+    with pytest.raises(ValueError, match="list"):
+        experts.mla_moe_combine([1.0], t, None, t)
+    with pytest.raises(ValueError, match="2 dimensions"):
+        experts.mla_fp8_matmul(t[0], t, t, t, t)
+
+
+def test_missing_native_binding_fails_loudly(monkeypatch):
+    """Without the built library or the native checks every call raises; there is no other path."""
+    import sys
+    monkeypatch.setattr(experts, "_bound", None)
+    monkeypatch.setitem(sys.modules, "sparse_mla_decode_front_b200._bind", None)
+    import sparse_mla_decode_front_b200 as pkg
+    monkeypatch.delattr(pkg, "_bind", raising=False)
+    t = torch.zeros(2, 16)
+    with pytest.raises(ImportError, match="_bind"):
+        experts.mla_moe_gather(t, t, t)

@@ -147,32 +147,39 @@ k_moe_gather(const T* x, const int32_t* row_of, int n_tokens, int K, int H, int 
 // ------------------------------------------------------------------ combine
 // 4096 tokens x 8 rows of 7168 bf16: 81 us, 6.5 TB/s (the measured copy rate; with the loads
 // evict-first 92 us, with eight choices in flight 120 us, two 81 us).
-// One thread: one unit of one token's output; the rows of kBatch choices are in flight at once.
+// A warp holds 32 units of one token. Its lanes fetch the token's row indices and weights side by
+// side, and the choices that have a row are taken from a ballot, kBatch rows in flight at a time:
+// a rank that holds an eighth of the experts finds one of eight choices here, and waits for two
+// latencies instead of one for each batch of indices and of rows.
 template <class T>
 __global__ void __launch_bounds__(kThreads)
-k_moe_combine(const T* rows, const int32_t* row_of, const float* weights,
-              int n_tokens, int K, int H, int R, int units, T* out) {
+k_moe_combine(const T* rows, const int32_t* row_of, const float* weights, int n_tokens, int K, int H, int R, int units,
+              int warps_per_row, T* out) {
     constexpr int kBatch = 4;
     griddep_launch();
     griddep_wait();
-    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const long long t = id / units;
-    const int u = (int)(id - t * units);
-    if (t >= n_tokens) return;
+    const int lane = threadIdx.x & 31;
+    const long long wid = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
+    const long long t = wid / warps_per_row;
+    const int u = (int)(wid - t * warps_per_row) * 32 + lane;
+    if (t >= n_tokens) return;   // uniform over the warp
+    const int my_row = lane < K ? row_of[t * K + lane] : -1;
+    const float my_w = lane < K && weights ? weights[t * K + lane] : 1.f;
+    unsigned left = __ballot_sync(0xffffffffu, (unsigned)my_row < (unsigned)R);
     float acc[kUnit] = {};
-    for (int k0 = 0; k0 < K; k0 += kBatch) {
+    while (left) {
         uint4 raw[kBatch][Unit<T>::kVecs];
         float w[kBatch];
         bool on[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int r = k0 + j < K ? row_of[t * K + k0 + j] : -1;
-            on[j] = (unsigned)r < (unsigned)R;
-            w[j] = 1.f;
-            if (on[j]) {
-                if (weights) w[j] = weights[t * K + k0 + j];
-                load_unit(raw[j], rows + (size_t)r * H + u * kUnit);
-            }
+        for (int j = 0; j < kBatch; ++j) {   // in the order of k
+            on[j] = left != 0;
+            const int k = on[j] ? __ffs(left) - 1 : 0;
+            left &= left - 1;
+            const int r = __shfl_sync(0xffffffffu, my_row, k);
+            w[j] = __shfl_sync(0xffffffffu, my_w, k);
+            on[j] = on[j] && u < units;
+            if (on[j]) load_unit(raw[j], rows + (size_t)r * H + u * kUnit);
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
@@ -185,6 +192,7 @@ k_moe_combine(const T* rows, const int32_t* row_of, const float* weights,
             }
         }
     }
+    if (u >= units) return;
     uint4 o[Unit<T>::kVecs];
 #pragma unroll
     for (int i = 0; i < kUnit / 2; ++i) Unit<T>::set(o, i, acc[2 * i], acc[2 * i + 1]);
@@ -273,16 +281,8 @@ k_moe_combine_backward(const T* dout, const T* rows, const int32_t* row_of,
 // One thread: one unit of one row. The gated activation in fp32: exp and the division by the
 // fast forms (2 ulp and exp's 2 + |1.16 g| ulp), far below e4m3's 2^-4.
 template <class T, bool GATED>
-__global__ void __launch_bounds__(kThreads)
-k_fp8_quantize(const T* x, int R, int C, int units, const int32_t* valid_rows,
-               uint8_t* q, float* scales) {
-    griddep_launch();
-    griddep_wait();
-    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const long long r = id / units;
-    const int u = (int)(id - r * units);
-    const int rows = valid_rows ? min(R, *valid_rows) : R;
-    const bool inside = r < rows && u * kUnit < C;
+__device__ __forceinline__ void quantize_row_unit(const T* x, long long r, int u, bool inside, int R, int C, uint8_t* q,
+                                                  float* scales) {
     uint4 rg[Unit<T>::kVecs] = {}, ru[Unit<T>::kVecs] = {};
     if (inside) {
         const T* p = x + (size_t)r * (GATED ? 2 * C : C) + u * kUnit;
@@ -308,6 +308,26 @@ k_fp8_quantize(const T* x, int R, int C, int units, const int32_t* valid_rows,
     if (u % kLanesPerScale == 0) scales[(size_t)(u / kLanesPerScale) * R + r] = scale;
 }
 
+// All rows: one unit a thread. With a count of valid rows (SOME) the grid is what the GPU holds at
+// once and strides over the valid rows: a rank that holds an eighth of the experts has capacity
+// for eight times its rows (8424 of 65536 rows x 2048: 20 us, 73 us when a block for every row
+// looked whether it was needed).
+template <class T, bool GATED, bool SOME>
+__global__ void __launch_bounds__(kThreads)
+k_fp8_quantize(const T* x, int R, int C, int units, const int32_t* valid_rows, uint8_t* q, float* scales) {
+    griddep_launch();
+    griddep_wait();
+    const int rows = SOME ? min(R, *valid_rows) : R;
+    long long first = (long long)blockIdx.x * kThreads;
+    do {
+        const long long r = (first + threadIdx.x) / units;
+        const int u = (int)(first + threadIdx.x - r * units);
+        if (SOME && first / units >= rows) return;   // uniform over the block
+        quantize_row_unit<T, GATED>(x, r, u, r < rows && u * kUnit < C, R, C, q, scales);
+        first += (long long)gridDim.x * kThreads;
+    } while (SOME);
+}
+
 // Units of a row: whole scale blocks when lanes share a scale, else the row's own.
 int row_units(int width, bool whole_blocks) {
     return whole_blocks ? (width + kScaleBlock - 1) / kScaleBlock * kLanesPerScale : width / kUnit;
@@ -328,9 +348,9 @@ cudaError_t gather_as(const void* x, const int32_t* row_of, int T_, int K, int H
 template <class T>
 cudaError_t combine_as(const void* rows, const int32_t* row_of, const float* w, int T_, int K, int H, int R, void* out,
                        cudaStream_t s) {
-    const int units = row_units(H, false);
-    return launch_pdl(k_moe_combine<T>, dim3(blocks_for(T_, units)), dim3(kThreads), 0, s,
-                      static_cast<const T*>(rows), row_of, w, T_, K, H, R, units, static_cast<T*>(out));
+    const int units = row_units(H, false), warps = (units + 31) / 32;
+    return launch_pdl(k_moe_combine<T>, dim3(blocks_for(T_, 32 * warps)), dim3(kThreads), 0, s,
+                      static_cast<const T*>(rows), row_of, w, T_, K, H, R, units, warps, static_cast<T*>(out));
 }
 
 template <class T>
@@ -345,23 +365,34 @@ cudaError_t combine_backward_as(const void* dout, const void* rows, const int32_
                       n, K, H, R, units, team, static_cast<T*>(drows), dw);
 }
 
-template <class T>
-cudaError_t quantize_as(const void* x, int R, int C, int gated, const int32_t* valid, void* q, float* scales,
-                        cudaStream_t s) {
+template <class T, bool GATED>
+cudaError_t quantize_as(const void* x, int R, int C, const int32_t* valid, void* q, float* scales, cudaStream_t s) {
     const int units = row_units(C, true);
-    const dim3 grid(blocks_for(R, units));
+    const unsigned blocks = blocks_for(R, units);
     const T* xt = static_cast<const T*>(x);
     uint8_t* qt = static_cast<uint8_t*>(q);
-    if (gated)
-        return launch_pdl(k_fp8_quantize<T, true>, grid, dim3(kThreads), 0, s, xt, R, C, units, valid, qt, scales);
-    return launch_pdl(k_fp8_quantize<T, false>, grid, dim3(kThreads), 0, s, xt, R, C, units, valid, qt, scales);
+    if (!valid)
+        return launch_pdl(k_fp8_quantize<T, GATED, false>, dim3(blocks), dim3(kThreads), 0, s, xt, R, C, units, valid, qt,
+                          scales);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k_fp8_quantize<T, GATED, true>, dim3(std::min(blocks, 16u * sms)), dim3(kThreads), 0, s, xt, R, C,
+                      units, valid, qt, scales);
+}
+template <class T>
+cudaError_t quantize_any(const void* x, int R, int C, int gated, const int32_t* valid, void* q, float* scales,
+                         cudaStream_t s) {
+    return gated ? quantize_as<T, true>(x, R, C, valid, q, scales, s) : quantize_as<T, false>(x, R, C, valid, q, scales, s);
 }
 
 }  // namespace
 
-// Blocks of 128 threads over rows x units: the grid's x extent holds 2^31 - 1.
+// Blocks of 128 threads over rows x units (of whole warps at most): the grid's x extent holds 2^31 - 1.
 bool moe_rows_fit(long long rows, int width) {
-    return (rows * row_units(width, true) + kThreads - 1) / kThreads < (1LL << 31);
+    const long long units = (row_units(width, true) + 31) / 32 * 32LL;
+    return (rows * units + kThreads - 1) / kThreads < (1LL << 31);
 }
 
 cudaError_t launch_moe_gather(const void* x, int dtype, const int32_t* row_of, int T, int K, int H, int R, void* rows,
@@ -395,9 +426,9 @@ cudaError_t launch_moe_combine_backward(const void* dout, const void* rows, int 
 cudaError_t launch_fp8_quantize(const void* x, int dtype, int R, int C, int gated, const int32_t* valid, void* q,
                                 float* scales, cudaStream_t s) {
     switch (dtype) {
-        case kDtypeBf16: return quantize_as<bf16>(x, R, C, gated, valid, q, scales, s);
-        case kDtypeFp16: return quantize_as<__half>(x, R, C, gated, valid, q, scales, s);
-        default: return quantize_as<float>(x, R, C, gated, valid, q, scales, s);
+        case kDtypeBf16: return quantize_any<bf16>(x, R, C, gated, valid, q, scales, s);
+        case kDtypeFp16: return quantize_any<__half>(x, R, C, gated, valid, q, scales, s);
+        default: return quantize_any<float>(x, R, C, gated, valid, q, scales, s);
     }
 }
 

@@ -145,17 +145,18 @@ k_moe_gather(const T* x, const int32_t* row_of, int n_tokens, int K, int H, int 
 }
 
 // ------------------------------------------------------------------ combine
-// 4096 tokens x 8 rows of 7168 bf16: 81 us, 6.5 TB/s (the measured copy rate; with the loads
-// evict-first 92 us, with eight choices in flight 120 us, two 81 us).
+// 4096 tokens x 8 rows of 7168 bf16: 79 us, 6.7 TB/s (the measured copy rate; with the loads
+// evict-first 92 us, with eight choices in flight 120 us). Eight blocks an SM (64 registers): with
+// 80 registers 81 us, and 70 us instead of 57 for 8192 tokens of which 8424 choices are here.
 // A warp holds 32 units of one token. Its lanes fetch the token's row indices and weights side by
 // side, and the choices that have a row are taken from a ballot, kBatch rows in flight at a time:
 // a rank that holds an eighth of the experts finds one of eight choices here, and waits for two
 // latencies instead of one for each batch of indices and of rows.
 template <class T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 6 : 8)
 k_moe_combine(const T* rows, const int32_t* row_of, const float* weights, int n_tokens, int K, int H, int R, int units,
               int warps_per_row, T* out) {
-    constexpr int kBatch = 4;
+    constexpr int kBatch = 8 / Unit<T>::kVecs;   // 128 bytes a lane
     griddep_launch();
     griddep_wait();
     const int lane = threadIdx.x & 31;

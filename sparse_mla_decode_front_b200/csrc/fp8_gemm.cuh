@@ -87,8 +87,16 @@ struct Tile {
 
 // All threads of the block; ends with a barrier. rows_per_tile rows x f_tiles feature tiles.
 __device__ __forceinline__ void build_groups(Groups& G, const Problem& p, int rows_per_tile, int f_tiles) {
-    for (int g = threadIdx.x; g <= p.groups; g += blockDim.x)
-        G.bound[g] = p.offsets ? min(max(p.offsets[g], 0), p.rows) : g * p.rows;   // without offsets: one group
+    if (!p.offsets) {   // one group
+        if (threadIdx.x == 0) {
+            G.bound[0] = G.start[0] = 0;
+            G.bound[1] = p.rows;
+            G.start[1] = (p.rows + rows_per_tile - 1) / rows_per_tile * f_tiles;
+        }
+        __syncthreads();
+        return;
+    }
+    for (int g = threadIdx.x; g <= p.groups; g += blockDim.x) G.bound[g] = min(max(p.offsets[g], 0), p.rows);
     __syncthreads();
     if (threadIdx.x < 32) {   // one warp, 32 groups at a time
         const int lane = threadIdx.x;
@@ -226,16 +234,19 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
         ptx::tma_prefetch_desc(&tma_w);
         ptx::tma_prefetch_desc(&tma_x);
     }
-    if (warp == 2) {
-        ptx::tmem_alloc(&tmem_slot, C::kTmemCols);
-        ptx::tmem_relinquish();
-    }
     griddep_wait();
     build_groups(G, p, BN, (p.n + BF - 1) / BF);
-    ptx::tc_fence_before();
-    __syncthreads();
-    ptx::tc_fence_after();
-    const uint32_t tmem = tmem_slot;
+    uint32_t tmem = 0;
+    if (warp > 0) {   // the first loads are issued while TMEM is allocated
+        if (warp == 2) {
+            ptx::tmem_alloc(&tmem_slot, C::kTmemCols);
+            ptx::tmem_relinquish();
+        }
+        ptx::tc_fence_before();
+        ptx::bar_sync_named(1, kFewThreads - 32);
+        ptx::tc_fence_after();
+        tmem = tmem_slot;
+    }
     const int tiles = G.start[p.groups];
     const int rank = p.split > 1 ? (int)ptx::cluster_ctarank() : 0;
     const int t0 = blockIdx.x / p.split, t_step = gridDim.x / p.split;   // with a split: one tile at most
@@ -574,6 +585,8 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
         ptx::tma_prefetch_desc(&tma_x);
         ptx::tma_prefetch_desc(&tma_w);
     }
+    griddep_wait();
+    build_groups(G, p, C::kRows, (p.n + kManyFeatures - 1) / kManyFeatures);
     if (warp == 3) {
         if (PAIR) {
             tmem_alloc_pair(&tmem_slot, 512);
@@ -582,8 +595,6 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
             ptx::tmem_relinquish();
         }
     }
-    griddep_wait();
-    build_groups(G, p, C::kRows, (p.n + kManyFeatures - 1) / kManyFeatures);
     ptx::tc_fence_before();
     __syncthreads();
     if (PAIR) ptx::cluster_sync_all();   // the peer's barriers are set up before anything arrives on them

@@ -41,11 +41,12 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), int size, dim3 grid, dim3 b
 }
 
 // How k_fp8_few splits `tiles` tiles of kb blocks: as far as every cluster is resident at once
-// and each CTA has two blocks or more. clusters[i]: resident clusters of 2^i CTAs.
+// and each CTA has two blocks or more. clusters[i]: resident clusters of 2^i CTAs. Returns the
+// split's logarithm.
 int few_split(long long tiles, int kb, const int (&clusters)[4]) {
     int i = 0;
     while (i < 3 && tiles <= clusters[i + 1] && kb >= 4 << i) ++i;
-    return 1 << i;
+    return i;
 }
 
 // What the host knows of one width of k_fp8_few on a device: resident clusters of 1, 2, 4 and 8
@@ -102,10 +103,10 @@ cudaError_t launch_few(const void* x, const void* w, const fp8::Problem& p, int 
     // Tiles there can be: a row tile for every BN rows and one more for each group that has rows.
     const long long tiles = ((long long)(p.rows - 1) / BN + std::min(p.groups, p.rows)) * ((p.n + fp8::BF - 1) / fp8::BF);
     fp8::Problem q = p;
-    q.split = few_split(tiles, p.kb, fd.clusters);
-    const dim3 grid((unsigned)std::min<long long>(tiles, sms_of(dev)) * q.split), block(fp8::kFewThreads);
-    if (q.split == 1) return launch_pdl(fp8::k_fp8_few<BN>, grid, block, C::kSmem, s, tw, tx, q);
-    return launch_cluster(fp8::k_fp8_few<BN>, q.split, grid, block, C::kSmem, s, tw, tx, q);
+    q.split_log2 = few_split(tiles, p.kb, fd.clusters);
+    const dim3 grid((unsigned)std::min<long long>(tiles, sms_of(dev)) << q.split_log2), block(fp8::kFewThreads);
+    if (q.split_log2 == 0) return launch_pdl(fp8::k_fp8_few<BN>, grid, block, C::kSmem, s, tw, tx, q);
+    return launch_cluster(fp8::k_fp8_few<BN>, 1 << q.split_log2, grid, block, C::kSmem, s, tw, tx, q);
 }
 
 template <bool PAIR>
@@ -140,7 +141,7 @@ cudaError_t few_cost(const fp8::Problem& p, int dev, int block, long long* cost)
     const cudaError_t e = few_device<BN>(dev, &fd);
     if (e != cudaSuccess) return e;
     const long long tiles = ((long long)p.rows + BN - 1) / BN * ((p.n + fp8::BF - 1) / fp8::BF);
-    const int split = few_split(tiles, p.kb, fd.clusters), sms = sms_of(dev);
+    const int split = 1 << few_split(tiles, p.kb, fd.clusters), sms = sms_of(dev);
     *cost = 600 + block * ((tiles + sms - 1) / sms) * ((p.kb + split - 1) / split);
     return cudaSuccess;
 }
@@ -189,7 +190,7 @@ bool fp8_gemm_fits(int rows, int groups, int n) {
 cudaError_t launch_fp8_gemm(const void* x, const float* xs, const void* w, const float* ws, const int32_t* offsets,
                             int rows, int groups, int n, int k, void* out, int dtype, int32_t* status,
                             cudaStream_t s) {
-    fp8::Problem p{xs, ws, offsets, rows, groups, n, k, (n + 127) / 128, (k + 127) / 128, out, dtype, status, 1};
+    fp8::Problem p{xs, ws, offsets, rows, groups, n, k, (n + 127) / 128, (k + 127) / 128, out, dtype, status, 0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

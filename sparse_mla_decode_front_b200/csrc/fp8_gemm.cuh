@@ -47,7 +47,7 @@ struct Problem {
     void* out;
     int dtype;
     int32_t* status;
-    int split;                   // k_fp8_few: CTAs (a cluster) that share a tile's K blocks
+    int split_log2;              // k_fp8_few: 2^split_log2 CTAs (a cluster) share a tile's K blocks
 };
 
 // Instruction descriptor, kind::f8f6f4: e4m3 A and B (both K-major), fp32 D.
@@ -248,9 +248,9 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
         tmem = tmem_slot;
     }
     const int tiles = G.start[p.groups];
-    const int rank = p.split > 1 ? (int)ptx::cluster_ctarank() : 0;
-    const int t0 = blockIdx.x / p.split, t_step = gridDim.x / p.split;   // with a split: one tile at most
-    const int kb0 = (int)((long long)p.kb * rank / p.split), kb1 = (int)((long long)p.kb * (rank + 1) / p.split);
+    const int split = 1 << p.split_log2, rank = split > 1 ? (int)ptx::cluster_ctarank() : 0;
+    const int t0 = blockIdx.x >> p.split_log2, t_step = gridDim.x >> p.split_log2;   // with a split: one tile at most
+    const int kb0 = (p.kb * rank) >> p.split_log2, kb1 = (p.kb * (rank + 1)) >> p.split_log2;
 
     if (warp == 0 && lane == 0) {
         // ---------------- TMA
@@ -390,7 +390,7 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
                 if (++buf == kBufs) { buf = 0; buf_phase ^= 1; }
             }
             if (!ok) break;
-            if (p.split > 1) {   // partial sums [row][feature] where the stages were: every load and UMMA is over
+            if (split > 1) {   // partial sums [row][feature] where the stages were: every load and UMMA is over
                 float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
                 for (int c = 0; c < BN; ++c) part[c * BF + quarter * 32 + lane] = acc[c];
@@ -437,26 +437,24 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
     }
     ptx::tc_fence_before();
     __syncthreads();
-    if (p.split > 1) {
+    if (split > 1) {
+        const Tile tl = t0 < tiles ? tile_at(G, p.groups, t0, BN, BF) : Tile{0, 0, 0, 0};
+        const int f = threadIdx.x % BF;
+        const uint32_t mine = ptx::smem_u32(smem) + 4 * f;
         ptx::cluster_sync_all();   // all ranks' partial sums are there
-        if (t0 < tiles) {
-            const Tile tl = tile_at(G, p.groups, t0, BN, BF);
-            const int f = threadIdx.x % BF;
-            const uint32_t mine = ptx::smem_u32(smem);
-            for (int c = rank + p.split * (threadIdx.x / BF); c < min(BN, tl.rows_left); c += p.split * (kFewThreads / BF)) {
-                float v[8];
+        for (int c = rank + split * (threadIdx.x / BF); c < min(BN, tl.rows_left); c += split * (kFewThreads / BF)) {
+            float v[8];
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    v[r] = r < p.split ? ld_cluster_f32(ptx::mapa_shared(mine, r) + 4 * (c * BF + f)) : 0.f;
-                float sum = v[0];
+            for (int r = 0; r < 8; ++r)
+                v[r] = r < split ? ld_cluster_f32(ptx::mapa_shared(mine, r) + 4 * c * BF) : 0.f;
+            float sum = v[0];
 #pragma unroll
-                for (int r = 1; r < 8; ++r) sum += v[r];
-                if (tl.f0 + f < p.n) {
-                    const size_t at = (size_t)(tl.row0 + c) * p.n + tl.f0 + f;
-                    if (p.dtype == kDtypeFp32) static_cast<float*>(p.out)[at] = sum;
-                    else if (p.dtype == kDtypeBf16) static_cast<bf16*>(p.out)[at] = __float2bfloat16_rn(sum);
-                    else static_cast<__half*>(p.out)[at] = __float2half_rn(sum);
-                }
+            for (int r = 1; r < 8; ++r) sum += v[r];
+            if (tl.f0 + f < p.n) {
+                const size_t at = (size_t)(tl.row0 + c) * p.n + tl.f0 + f;
+                if (p.dtype == kDtypeFp32) static_cast<float*>(p.out)[at] = sum;
+                else if (p.dtype == kDtypeBf16) static_cast<bf16*>(p.out)[at] = __float2bfloat16_rn(sum);
+                else static_cast<__half*>(p.out)[at] = __float2half_rn(sum);
             }
         }
         ptx::cluster_sync_all();   // no rank leaves while its sums are read

@@ -172,8 +172,8 @@ __device__ __forceinline__ bool issue_blocks(int first, int tiles, int kb, uint6
     for (int i = 0; i < tiles; ++i) {
         const uint32_t idesc = idesc_of(i);
         for (; next < kb; next += 2) {
-            if (!ptx::mbar_wait(&full_bar[stage], phase, status) ||
-                !ptx::mbar_wait(&acc_empty[buf], buf_phase ^ 1, status))
+            if (!ptx::mbar_wait_spin(&full_bar[stage], phase, status) ||
+                !ptx::mbar_wait_spin(&acc_empty[buf], buf_phase ^ 1, status))
                 return false;
             ptx::tc_fence_after();
             issue(idesc, stage, buf);
@@ -614,7 +614,7 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
                 const int x_row = tl.row0 + rank * kManyRows;
                 const int w_row = tl.g * p.n + tl.f0 + (PAIR ? rank * (width_of(tl.f0) / 2) : 0);
                 for (int kb = 0; kb < p.kb; ++kb) {
-                    if (!ptx::mbar_wait(&empty_bar[stage], phase ^ 1, p.status)) { abort_flag = 1; goto loads_done; }
+                    if (!ptx::mbar_wait_spin(&empty_bar[stage], phase ^ 1, p.status)) { abort_flag = 1; goto loads_done; }
                     if (*(volatile int*)&abort_flag) goto loads_done;
                     unsigned char* x_s = smem + stage * C::kStageBytes;
                     if (PAIR) {
@@ -635,7 +635,7 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
             if (rank == 0)   // every load lands before shared memory is released (a pair leaves together)
                 for (int i = 0; i < S && i < issued; ++i) {
                     if (--stage < 0) { stage = S - 1; phase ^= 1; }
-                    ptx::mbar_wait(&full_bar[stage], phase, p.status);
+                    ptx::mbar_wait_spin(&full_bar[stage], phase, p.status);
                 }
         } else if ((warp == 1 || warp == 2) && lane == 0 && rank == 0) {
             // ---------------- UMMA: every second K block each
@@ -657,7 +657,7 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
                 [](uint64_t* bar) { PAIR ? umma_commit_pair(bar) : ptx::umma_commit(bar); });
             if (!ok) abort_flag = 1;
             PAIR ? umma_commit_leader(&mma_done) : ptx::umma_commit(&mma_done);   // all UMMAs complete before TMEM is released
-            ptx::mbar_wait(&mma_done, 0, p.status);
+            ptx::mbar_wait_spin(&mma_done, 0, p.status);
         } else if (warp == 3) {
             // ---------------- scales: 128 row scales and two weight scales a block, kScales blocks
             // at a time and one such batch ahead (a load's latency is longer than a block's product,
@@ -670,7 +670,7 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
                 const int r0 = tl.row0 + rank * kManyRows + lane;
                 const float* ws = p.ws + ((size_t)tl.g * p.nb + min((tl.f0 >> 7) + (lane & 1), p.nb - 1)) * p.kb + (lane >> 1);
                 for (int k0 = 0; k0 < p.kb; k0 += kScales) {
-                    if (!ptx::mbar_wait(&sc_empty[slot], phase ^ 1, p.status)) { abort_flag = 1; ok = false; break; }
+                    if (!ptx::mbar_wait_spin(&sc_empty[slot], phase ^ 1, p.status)) { abort_flag = 1; ok = false; break; }
                     const int nk = min(kScales, p.kb - k0);
                     for (int j = 0; j < nk; ++j)
 #pragma unroll
@@ -712,14 +712,14 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
             // 32 columns load while 32 are added, the last 32 of a block while the next one's
             // first load.
             float s = 0.f, s_next = 0.f;
-            if (ptx::mbar_wait(&sc_full[slot], sc_phase, p.status))
+            if (ptx::mbar_wait_spin(&sc_full[slot], sc_phase, p.status))
                 s_next = my_x[slot * kScales * kManyRows] * my_w[slot * kScales * 2];
             else
                 ok = false;
             for (int kb = 0; ok && kb < p.kb; ++kb) {
                 const float s_prev = s;
                 s = s_next;
-                if (!ptx::mbar_wait(&acc_full[q], acc_phase, p.status)) {
+                if (!ptx::mbar_wait_spin(&acc_full[q], acc_phase, p.status)) {
                     ok = false;
                     break;
                 }
@@ -732,7 +732,7 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
                     if (lane == 0) ptx::mbar_arrive(&sc_empty[slot]);
                     slot ^= 1;
                     if (slot == 0) sc_phase ^= 1;
-                    if (kb + 1 < p.kb && !ptx::mbar_wait(&sc_full[slot], sc_phase, p.status)) ok = false;
+                    if (kb + 1 < p.kb && !ptx::mbar_wait_spin(&sc_full[slot], sc_phase, p.status)) ok = false;
                 }
                 if (kb + 1 < p.kb)
                     s_next = my_x[(slot * kScales + j) * kManyRows] * my_w[(slot * kScales + j) * 2];

@@ -65,10 +65,25 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 }
 // Wait until the phase with the given parity has completed. Returns false (and
 // flags the status word) if it has not within kWaitTimeoutNs.
-// The clock is read after every kSpins probes only: globaltimer is slow to read, and a read
-// between probes delays the waiter by more than the probe itself.
-constexpr int kSpins = 64;
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (globaltimer() - t0 > kWaitTimeoutNs) {
+            if (status) atomicOr(status, MLA_DEV_WAIT_TIMEOUT);
+            return false;
+        }
+    }
+}
+// The same wait with the clock read after every kSpins probes only: globaltimer is slow to read,
+// and a read between probes delays a waiter whose phase completes meanwhile. For chains of short
+// blocks with one waiter a role (the 8-bit products: 4096 x 7168 x 16384 in 565 us with the wait
+// above, 546 with this one). Where several warps of an SM wait most of the time, the reads leave the
+// issue slots to the warps that work: the attention core takes 153 us with the wait above, 174 with
+// this one.
+constexpr int kSpins = 64;
+__device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, int32_t* status) {
     for (int i = 0; i < kSpins; ++i)
         if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer();

@@ -80,7 +80,8 @@ int mla_moe_sort(const int32_t* topk_idx, const void* affinities, int n_tokens, 
                  void* stream);
 
 /* rows[row_of[t, k]] = x[t] for every choice that has a row; other rows are left as they
- * were. Its gradient is mla_moe_combine with weights NULL.
+ * were. row_of names a row once (as mla_moe_sort writes it; a row named twice would take
+ * one or the other). Its gradient is mla_moe_combine with weights NULL.
  *
  *   x       [n_tokens, hidden] of `dtype`
  *   rows    [n_rows, hidden] of `dtype` when scales is NULL; else e4m3, with

@@ -30,7 +30,12 @@ int check(std::initializer_list<const void*> tensors, std::initializer_list<cons
 }
 bool misaligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
 bool dtype_ok(int dtype) { return dtype >= MLA_DTYPE_BF16 && dtype <= MLA_DTYPE_FP32; }
-int done(cudaError_t e) { return cuda_call_failed(e) ? MLA_ERR_CUDA : MLA_OK; }
+// A failed launch is reported here and not left behind for the caller's next CUDA check.
+int done(cudaError_t e) {
+    if (!cuda_call_failed(e)) return MLA_OK;
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+}
 cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 bool sort_dims_ok(int T, int K, int E) {

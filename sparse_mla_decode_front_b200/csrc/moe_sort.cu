@@ -40,8 +40,8 @@ struct Args {
 };
 
 __device__ __forceinline__ int key_of(const Args& a, int i) {
-    const int e = a.idx[i] - a.first;
-    return (unsigned)e < (unsigned)a.E ? e : a.E;
+    const long long e = (long long)a.idx[i] - a.first;   // any int32 may be there
+    return e >= 0 && e < a.E ? (int)e : a.E;
 }
 
 // Routing weights of the tokens of block `b` of the weight blocks: a lane for each choice, so

@@ -79,7 +79,8 @@ def random_rows(T, K, R, seed, missing=0.2):
 # ------------------------------------------------------------------ sort
 SORTS = [(1, 1, 1, 0, 1), (1, 8, 256, 0, 256), (128, 8, 256, 0, 256), (37, 5, 96, 48, 48), (512, 8, 256, 0, 256),
          (513, 8, 256, 0, 256), (300, 32, 1024, 0, 1024), (129, 32, 1024, 0, 1024), (12289, 8, 256, 64, 32),
-         (4097, 1, 64, 63, 1), (1, 32, 64, 8, 8), (700, 7, 80, 0, 80)]
+         (4097, 1, 64, 63, 1), (1, 32, 64, 8, 8), (700, 7, 80, 0, 80),
+         (100, 32, 1024, 0, 1024), (128, 32, 1024, 512, 512)]
 
 
 @pytest.mark.parametrize("T,K,total,first,E", SORTS)
@@ -95,7 +96,7 @@ def test_sort_matches_oracle(T, K, total, first, E):
         within(f64(w), ref, np.abs(ref) * (K + 2) * 2.0 ** -24, "weights")
 
 
-@pytest.mark.parametrize("kind", ["none_here", "one_expert", "last_expert", "same_choice_twice"])
+@pytest.mark.parametrize("kind", ["none_here", "one_expert", "last_expert", "same_choice_twice", "extremes"])
 @pytest.mark.parametrize("T", [3, 2000])
 def test_sort_skewed(kind, T):
     idx = torch.randint(0, 64, (T, 4), generator=gen(1), device="cuda", dtype=torch.int32)
@@ -105,10 +106,13 @@ def test_sort_skewed(kind, T):
         idx.fill_(17)
     elif kind == "last_expert":
         idx.fill_(63)
+    elif kind == "extremes":
+        idx[:, 0], idx[:, 2] = -2 ** 31, 2 ** 31 - 1
     else:
         idx[:, 1] = idx[:, 0]
-    out, _ = run_sort(idx, 0, 64)
-    want = X.sort(idx.cpu().numpy(), 0, 64)
+    first, E = (40, 16) if kind == "extremes" else (0, 64)
+    out, _ = run_sort(idx, first, E)
+    want = X.sort(idx.cpu().numpy(), first, E)
     for k, v in out.items():
         assert np.array_equal(v.cpu().numpy(), want[k]), k
 
@@ -353,6 +357,26 @@ def test_grouped_matmul_tilings(N, K):
     for e, c in enumerate(counts):
         part = slice(off[e], off[e + 1])
         check_product(out[part], x[part], xs[:, part], w[e], ws[e], torch.bfloat16, f"expert {e}")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(2560, 2048, 4096), (2500, 2000, 4112), (512, 10240, 4096), (4000, 7152, 2064)])
+def test_matmul_a_few_tiles_past_whole_waves(M, N, K, dtype):
+    # tiles a few past whole waves of CTA pairs: every tile once, and no row behind the last
+    x, xs = make_operand(M, K, M + N)
+    w, ws = make_weight(1, N, K, N + K)
+    buf = filled(M + 2, N, dtype=dtype)
+    G.mla_fp8_matmul(x, xs, w[0], ws[0], buf[1:M + 1])
+    torch.cuda.synchronize()
+    assert untouched(buf[0]) and untouched(buf[-1])
+    rng = np.random.default_rng(M)
+    edges = [r for b in range(0, M, 256) for r in (b - 1, b, b + 128) if 0 <= r < M] + [M - 1]
+    at = torch.tensor(sorted(set(edges + rng.integers(0, M, 60).tolist())), device="cuda")
+    check_product(buf[1:M + 1][at], x[at], xs[:, at].contiguous(), w[0], ws[0], dtype)
+    assert bool(torch.isfinite(buf[1:M + 1].float()).all())
+    again = filled(M, N, dtype=dtype)
+    G.mla_fp8_matmul(x, xs, w[0], ws[0], again)
+    assert torch.equal(again, buf[1:M + 1])
 
 
 def test_offsets_beyond_32_bits():

@@ -80,8 +80,8 @@ int mla_moe_sort(const int32_t* topk_idx, const void* affinities, int n_tokens, 
                  void* stream);
 
 /* rows[row_of[t, k]] = x[t] for every choice that has a row; other rows are left as they
- * were. row_of names a row once (as mla_moe_sort writes it; a row named twice would take
- * one or the other). Its gradient is mla_moe_combine with weights NULL.
+ * were. row_of names a row at most once, as mla_moe_sort writes it (what a row named twice
+ * holds is not defined). Its gradient is mla_moe_combine with weights NULL.
  *
  *   x       [n_tokens, hidden] of `dtype`
  *   rows    [n_rows, hidden] of `dtype` when scales is NULL; else e4m3, with
@@ -107,6 +107,8 @@ int mla_moe_combine(const void* rows, int dtype, const int32_t* row_of, const fl
 /* Gradients of mla_moe_combine:
  *   grad_rows[row_of[t, k]] = weights[t, k] * grad_out[t]   (rows of no choice: left as they were)
  *   grad_weights[t, k]      = <grad_out[t], rows[row_of[t, k]]>, fp32; 0 for a choice without a row
+ * row_of names a row at most once, as mla_moe_sort writes it (the gradients of a row named
+ * twice are not added up; what grad_rows then holds there is not defined).
  * grad_rows or grad_weights may be NULL when it is not wanted (not both); weights may be
  * NULL (ones), and rows may be NULL when grad_weights is. */
 int mla_moe_combine_backward(const void* grad_out, const void* rows, int dtype, const int32_t* row_of,

@@ -599,8 +599,9 @@ k_fp8_many(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CU
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const int tiles = G.start[p.groups];
-    // Features of a tile, a multiple of 16: the UMMA's N. Of a pair's, the first half are the leader's weight rows.
-    auto width_of = [&](int f0) { return min(kManyFeatures, p.n - f0); };
+    // Features of a tile, the UMMA's N: a multiple of 16, and of 32 in a pair, whose first half are the leader's
+    // weight rows (of those behind the last feature, zeros, nothing is stored).
+    auto width_of = [&](int f0) { return min(kManyFeatures, PAIR ? (p.n - f0 + 31) & ~31 : p.n - f0); };
 
     if (warp < 4) {
         // 128 x 72 + 256 x 216 registers = 384 x 168, what the block was launched with

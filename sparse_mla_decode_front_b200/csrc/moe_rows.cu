@@ -205,9 +205,12 @@ k_moe_combine(const T* rows, const int32_t* row_of, const float* weights, int n_
 // with ordinary loads and stores 134 us).
 // A team of `team` warps takes one choice: grad_row = w grad_out[t], and the dot product of
 // grad_out[t] with the row. Blocks of 8 warps hold 8 / team neighbouring choices, so the
-// choices of a token read its grad_out from L1 / L2. Few choices: 8 warps each, for latency;
-// many: one.
+// choices of a token read its grad_out from L1 / L2. Few choices take
+// more warps each, for latency, up to 16 warps an SM (teams of 8 / 4 / 2 / 1, us, rows of 7168: 296
+// choices 3.4 / 4.2 / 4.5 / 6.6, 584 5.5 / 4.4 / 6.4 / 10.5, 1024 9.5 / 7.5 / 7.1 / 10.9, 2048 16.9 /
+// 13.0 / 12.2 / 11.8, 16384 138 / 98 / 89 / 84; rows of 1024: 1024 choices 6.2 / 3.8 / 2.6 / 2.8).
 constexpr int kBackWarps = 8;
+constexpr int kBackTeamWarps = 16 * 148;   // 16 an SM
 template <class T>
 __global__ void __launch_bounds__(32 * kBackWarps)
 k_moe_combine_backward(const T* dout, const T* rows, const int32_t* row_of,
@@ -277,10 +280,18 @@ k_moe_combine_backward(const T* dout, const T* rows, const int32_t* row_of,
 }
 
 // ------------------------------------------------------------------ quantise
-// 32768 x 2048 of bf16 [g | u]: 62 us, 5.4 TB/s (evict-first loads 66 us, two units a thread 66 us,
-// blocks of 16 rows x 128 columns 66 us; 59 us without the scales' scattered 4-byte stores).
+// 32768 x 2048 of bf16 [g | u]: 62 us, 5.4 TB/s (evict-first loads, two units a thread or blocks of 16
+// rows x 128 columns: 4 us more; 3 us of it are the scales' scattered 4-byte stores).
 // One thread: one unit of one row. The gated activation in fp32: exp and the division by the
 // fast forms (2 ulp and exp's 2 + |1.16 g| ulp), far below e4m3's 2^-4.
+// Below a gate of -80, where 1 + exp(-g) is exp(-g) in fp32, the quotient is g exp(g): from about -87
+// on the fast division gives 0 for a divisor past 2^126, and a product with a large u still counts.
+// In two halves, so that no factor leaves fp32's range before the result does. (Such a unit is rare and
+// is read again: 62 us, against 60.5 without it, 64.6 with the unit held and 72 with every gate this way.)
+__device__ __forceinline__ float far_gate(float g, float u) {
+    const float h = __expf(0.5f * g);
+    return (g * h) * (h * u);
+}
 template <class T, bool GATED>
 __device__ __forceinline__ void quantize_row_unit(const T* x, long long r, int u, bool inside, int R, int C, uint8_t* q,
                                                   float* scales) {
@@ -290,17 +301,29 @@ __device__ __forceinline__ void quantize_row_unit(const T* x, long long r, int u
         load_unit(rg, p);
         if (GATED) load_unit(ru, p + C);
     }
-    float v[kUnit];
+    float v[kUnit], low = 0.f;
 #pragma unroll
     for (int i = 0; i < kUnit / 2; ++i) {
         float2 g = Unit<T>::pair(rg, i);
         if (GATED) {
             const float2 m = Unit<T>::pair(ru, i);
+            low = fminf(low, fminf(g.x, g.y));
             g.x = __fdividef(g.x, 1.f + __expf(-g.x)) * m.x;
             g.y = __fdividef(g.y, 1.f + __expf(-g.y)) * m.y;
         }
         v[2 * i] = g.x;
         v[2 * i + 1] = g.y;
+    }
+    if (GATED && low < -80.f) {
+        const T* p = x + (size_t)r * (2 * C) + u * kUnit;
+        load_unit(rg, p);
+        load_unit(ru, p + C);
+#pragma unroll
+        for (int i = 0; i < kUnit / 2; ++i) {
+            const float2 g = Unit<T>::pair(rg, i), m = Unit<T>::pair(ru, i);
+            if (g.x < -80.f) v[2 * i] = far_gate(g.x, m.x);
+            if (g.y < -80.f) v[2 * i + 1] = far_gate(g.y, m.y);
+        }
     }
     float scale;
     const uint4 o = quantize_unit(v, &scale);
@@ -359,7 +382,8 @@ cudaError_t combine_backward_as(const void* dout, const void* rows, const int32_
                                 int K, int H, int R, void* drows, float* dw, cudaStream_t s) {
     const long long n = (long long)T_ * K;
     const int units = row_units(H, false);
-    const int team = n < 592 ? 8 : 1;
+    int team = kBackWarps;
+    while (team > 1 && n * team > kBackTeamWarps) team >>= 1;
     const long long per_block = kBackWarps / team;
     return launch_pdl(k_moe_combine_backward<T>, dim3((unsigned)((n + per_block - 1) / per_block)),
                       dim3(32 * kBackWarps), 0, s, static_cast<const T*>(dout), static_cast<const T*>(rows), row_of, w,

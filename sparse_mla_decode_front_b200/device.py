@@ -198,7 +198,8 @@ class ExpertLayer:
     The experts of this rank are ``w_up`` [E, 2 * width, hidden] and ``w_down`` [E, hidden, width]
     (e4m3, scales [E, ceil(n / 128), ceil(k / 128)]), global ids from ``first_expert`` on;
     ``router_weights`` [hidden, all experts]. Choices of other ranks' experts are left out: the
-    outputs of all ranks add up to the layer's. ``run`` allocates nothing and can be captured."""
+    outputs of all ranks add up to the layer's. ``run`` allocates nothing and can be captured; it
+    works in the layer's own buffers, so one run at a time."""
 
     def __init__(self, n_tokens: int, gamma, router_weights, w_up, w_up_scales, w_down, w_down_scales, top_k: int,
                  first_expert: int = 0, router_bias=None, act: str = "sigmoid", normalize: bool = True,

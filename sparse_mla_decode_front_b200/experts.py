@@ -68,7 +68,8 @@ def mla_moe_sort(topk_idx, expert_offsets, row_of, source_of, workspace=None, fi
 
 def mla_moe_gather(x, row_of, rows, scales: Optional[torch.Tensor] = None, stream=None) -> None:
     """``rows``[row_of[t, k]] = ``x``[t]; with ``scales`` [ceil(H / 128), R] fp32, ``rows`` [R, H]
-    is e4m3. Its gradient is ``mla_moe_combine`` without weights."""
+    is e4m3. ``row_of`` names a row at most once, as ``mla_moe_sort`` writes it. Its gradient is
+    ``mla_moe_combine`` without weights."""
     rc = (_bound or _native()).moe_gather(x, row_of, rows, scales, stream)
     if rc:
         raise MlaError(rc, "mla_moe_gather")
@@ -87,7 +88,8 @@ def mla_moe_combine_backward(grad_out, rows, row_of, weights: Optional[torch.Ten
                              stream=None) -> None:
     """Gradients of ``mla_moe_combine``: ``grad_rows`` [R, H] (rows of no choice are left as they
     were) and ``grad_weights`` [T, K] fp32; either may be None. ``rows`` may be None without
-    ``grad_weights``."""
+    ``grad_weights``. ``row_of`` names a row at most once: the gradients of a row named twice are
+    not added up."""
     rc = (_bound or _native()).moe_combine_backward(grad_out, rows, row_of, weights, grad_rows, grad_weights, stream)
     if rc:
         raise MlaError(rc, "mla_moe_combine_backward")

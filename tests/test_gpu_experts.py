@@ -218,6 +218,23 @@ def test_quantize_gated_far_gates():
     np.testing.assert_allclose(f64(q.float()[1]) * f64(scales)[0, 1], 600.0, rtol=2.0 ** -20)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantize_gated_far_gates_and_large_values(dtype):
+    # silu(g) is below fp32's normal range, its product with u is not
+    C = 64
+    x = torch.empty(3, 2 * C, device="cuda")
+    x[0, :C] = -torch.linspace(81, 165, C, device="cuda")
+    x[1, :C] = -torch.linspace(86, 90, C, device="cuda")
+    x[2, :C] = torch.linspace(-90, 8, C, device="cuda")
+    x[:, C:] = torch.linspace(1e38, 3e38, C, device="cuda")
+    x[2, C:] = 4e37
+    x = x.to(dtype)
+    q, scales = filled(3, C, dtype=E4M3), filled(1, 3, dtype=torch.float32)
+    G.mla_fp8_quantize(x, q, scales, True)
+    # exp of half the gate within 2 + 1.16 * 83 steps (2^-23), taken twice, and three products
+    check_quantized(q.float(), scales, X.gated(f64(x)), (2 * (2 + 1.16 * 83) + 3) * 2.0 ** -23)
+
+
 @pytest.mark.parametrize("valid", [-3, 0, 1, 77, 100, 5000])
 def test_quantize_only_the_valid_rows(valid):
     x = torch.randn(100, 144, generator=gen(9), device="cuda").to(torch.bfloat16)
@@ -267,6 +284,22 @@ def test_combine_and_gradient(T, K, H, R, weighted, dtype):
     G.mla_moe_combine_backward(dout, None, row_of, w, gr1, None)
     G.mla_moe_combine_backward(dout, rows, row_of, w, None, gw1)
     assert torch.equal(gr1.view(torch.uint8), gr.view(torch.uint8)) and torch.equal(gw1, gw)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("n", [296, 297, 592, 593, 1184, 1185])
+def test_combine_backward_at_every_team_size(n, dtype):
+    T, K, H = n, 1, 16 * 37
+    rows, dout = (torch.randn(T, H, generator=gen(n + i), device="cuda").to(dtype) for i in range(2))
+    row_of = random_rows(T, K, T, 4)
+    gr, gw = filled(T, H, dtype=dtype), filled(T, K, dtype=torch.float32)
+    G.mla_moe_combine_backward(dout, rows, row_of, None, gr, gw)
+    want_r, want_w = X.combine_backward(f64(dout), f64(rows), row_of.cpu().numpy(), None)
+    used = ~np.isnan(want_r[:, 0])
+    assert np.array_equal(f64(gr)[used], want_r[used])
+    assert untouched(gr[~torch.from_numpy(used).cuda()])
+    _, mag_w = X.combine_backward(np.abs(f64(dout)), np.abs(f64(rows)), row_of.cpu().numpy(), None)
+    within(f64(gw), want_w, mag_w * H * 2.0 ** -24, "grad_weights")
 
 
 def test_gather_gradient_is_the_unweighted_combine():

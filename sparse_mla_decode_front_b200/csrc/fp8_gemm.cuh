@@ -475,7 +475,7 @@ k_fp8_few(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUt
 // half of the weight rows, and each one's tensor core reads both halves). A block then takes
 // 32 KB of operands a CTA instead of 48, and an SM takes in about 64 bytes a clock from L2
 // (390 ns a block measured for the single CTA with the drain left out). Measured in a loop (the
-// 1000 W cap holds the clock at 1.54 GHz): 4096 x 7168 x 16384 530 us, 1.8 PFLOP/s, against 579 us
+// 1000 W cap holds the clock at 1.54 GHz): 4096 x 7168 x 16384 530 - 550 us, 1.8 PFLOP/s, against 579 us
 // for single CTAs. But a group's last tile is half empty on average, and of 128 rows that costs less
 // than of 256: 8191 rows over 32 experts (3 to 2156 each), 4096 x 7168: 369 - 441 us single, 439 - 480
 // us in pairs. Hence pairs for the plain product, single CTAs for groups.

@@ -273,8 +273,10 @@ void chunking(long long n, int* chunks, int* items) {
     *chunks = (int)((n + *items - 1) / *items);
 }
 
+// A launch may use 48 KB of shared memory without asking, its static and dynamic parts together.
+constexpr size_t kStaticSmem = 256;   // the kernels' static arrays and a margin (144 bytes by ptxas)
 cudaError_t allow_smem(const void* kernel, size_t bytes) {
-    return bytes > 48 * 1024
+    return bytes + kStaticSmem > 48 * 1024
                ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
                : cudaSuccess;
 }
@@ -303,11 +305,10 @@ cudaError_t launch_moe_sort(const int32_t* idx, const bf16* aff, int T, int K, i
         if (e != cudaSuccess) return e;
         return launch_pdl(k_moe_sort_single, dim3(1 + weight_blocks), dim3(kThreads), smem, s, a);
     }
-    chunking(a.n, &a.chunks, &a.chunk_items);
-    cudaError_t e = launch_pdl(k_moe_sort_count, dim3(a.chunks + weight_blocks), dim3(kThreads),
-                               sizeof(int) * (E + 1), s, a);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_moe_sort_place), smem_place);
     if (e != cudaSuccess) return e;
-    e = allow_smem(reinterpret_cast<const void*>(k_moe_sort_place), smem_place);
+    chunking(a.n, &a.chunks, &a.chunk_items);
+    e = launch_pdl(k_moe_sort_count, dim3(a.chunks + weight_blocks), dim3(kThreads), sizeof(int) * (E + 1), s, a);
     if (e != cudaSuccess) return e;
     return launch_pdl_mode(true, k_moe_sort_place, dim3(a.chunks), dim3(kThreads), smem_place, s, a);
 }

@@ -13,9 +13,11 @@
 // for the routing weights beside it; more are cut into chunks, a first launch counting each
 // chunk's bins and a second placing the chunk behind the chunks before it.
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "launch.h"
+#include "moe_experts.h"
 
 namespace mla {
 namespace {
@@ -26,6 +28,7 @@ constexpr int kPerLane = 4;                            // choices a lane holds i
 constexpr int kPassItems = kThreads * kPerLane;        // choices of one pass of a block
 constexpr int kSingleItems = kPassItems;
 constexpr int kMaxChunks = 256;                        // chunks (blocks) of the two-launch form
+constexpr int kMaxExperts = MLA_MOE_MAX_EXPERTS;
 constexpr unsigned kAll = 0xffffffffu;
 
 struct Args {
@@ -273,12 +276,23 @@ void chunking(long long n, int* chunks, int* items) {
     *chunks = (int)((n + *items - 1) / *items);
 }
 
-// A launch may use 48 KB of shared memory without asking, its static and dynamic parts together.
-constexpr size_t kStaticSmem = 256;   // the kernels' static arrays and a margin (144 bytes by ptxas)
-cudaError_t allow_smem(const void* kernel, size_t bytes) {
-    return bytes + kStaticSmem > 48 * 1024
-               ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
-               : cudaSuccess;
+// A launch may use 48 KB of shared memory without asking, its static and dynamic parts together, and
+// more up to the kernel's limit on the device. The limit is set once, to what the most experts take:
+// it belongs to the kernel and not to a launch, so one that followed each call's size would be
+// lowered by one host thread between another's request and its launch.
+constexpr int kMaxDevices = 64;
+template <void (*KERNEL)(Args), int ARRAYS>
+cudaError_t allow_smem() {
+    static std::atomic<bool> set[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool keep = dev >= 0 && dev < kMaxDevices;
+    if (keep && set[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem_bytes(ARRAYS, kMaxExperts + 1));
+    if (keep && e == cudaSuccess) set[dev].store(true, std::memory_order_release);
+    return e;
 }
 
 }  // namespace
@@ -301,11 +315,11 @@ cudaError_t launch_moe_sort(const int32_t* idx, const bf16* aff, int T, int K, i
     const int weight_blocks = aff ? (T + weight_tokens - 1) / weight_tokens : 0;
     const size_t smem = smem_bytes(2, E + 1), smem_place = smem_bytes(4, E + 1);
     if (a.n <= kSingleItems) {
-        cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_moe_sort_single), smem);
+        const cudaError_t e = allow_smem<k_moe_sort_single, 2>();
         if (e != cudaSuccess) return e;
         return launch_pdl(k_moe_sort_single, dim3(1 + weight_blocks), dim3(kThreads), smem, s, a);
     }
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_moe_sort_place), smem_place);
+    cudaError_t e = allow_smem<k_moe_sort_place, 4>();
     if (e != cudaSuccess) return e;
     chunking(a.n, &a.chunks, &a.chunk_items);
     e = launch_pdl(k_moe_sort_count, dim3(a.chunks + weight_blocks), dim3(kThreads), sizeof(int) * (E + 1), s, a);

@@ -70,7 +70,13 @@ def build_bind(force: bool = False, verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    """The library, which needs nvcc alone, and then the Python binding's native part."""
+    lib = build_lib(force, verbose, extra)
     build_bind(force, verbose)
+    return lib
+
+
+def build_lib(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and up_to_date():
         return LIB
     out_dir = os.path.join(HERE, "_build")

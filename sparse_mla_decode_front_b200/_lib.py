@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsparse_mla_decode.so")
@@ -130,6 +131,13 @@ def lib() -> ctypes.CDLL:
             fn.argtypes = args
         _lib = l
     return _lib
+
+
+def bind_tag() -> str:
+    """What the native part of the experts binding has to be built for: it uses torch's inline C++ and
+    Python's C API, and neither's layout is the same in another version."""
+    import torch
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
 
 
 def status_string(code: int) -> str:

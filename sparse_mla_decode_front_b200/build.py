@@ -5,7 +5,8 @@
 compiles every ``csrc/*.cu`` into ``libsparse_mla_decode.so`` next to this
 file (cudart linked statically), and ``csrc/bind.cpp`` (g++, against torch's
 headers) into ``_bind.so``, the experts binding's native argument checks.
-Rebuilds only when a source is newer.
+Rebuilds only when a source is newer, and ``_bind.so`` also when torch or
+Python is another one than it was built for.
 """
 from __future__ import annotations
 
@@ -50,8 +51,15 @@ def build_bind(force: bool = False, verbose: bool = False) -> str:
     """``_bind.so``: it calls the library through addresses it is given, and links torch only."""
     src = os.path.join(HERE, "csrc", "bind.cpp")
     used = [src, os.path.join(ROOT, "include", "moe_experts.h")]
+    from ._lib import bind_tag
+    tag, tag_file = bind_tag(), os.path.join(HERE, "_build", "bind.tag")   # what the last _bind.so was built for
     if not force and os.path.exists(BIND) and all(os.path.getmtime(f) <= os.path.getmtime(BIND) for f in used):
-        return BIND
+        try:
+            with open(tag_file) as f:
+                if f.read() == tag:
+                    return BIND
+        except OSError:
+            pass
     import torch
     site = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
@@ -59,13 +67,16 @@ def build_bind(force: bool = False, verbose: bool = False) -> str:
                os.path.join(site, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
     tmp = BIND + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DBIND_TAG="{tag}"', "-I", os.path.join(ROOT, "include"),
            *[a for d in include for a in ("-isystem", d)], src, "-o", tmp, "-L" + os.path.join(site, "lib"),
            "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, BIND)
+    os.makedirs(os.path.dirname(tag_file), exist_ok=True)
+    with open(tag_file, "w") as f:
+        f.write(tag)
     return BIND
 
 

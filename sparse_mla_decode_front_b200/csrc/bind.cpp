@@ -365,4 +365,10 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_bind", "native argument marshal
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__bind(void) { return PyModule_Create(&g_module); }
+// The module says which torch and Python its inline layouts are from (BIND_TAG, given by the build);
+// experts.py compares that with the ones that load it.
+PyMODINIT_FUNC PyInit__bind(void) {
+    PyObject* m = PyModule_Create(&g_module);
+    if (m && PyModule_AddStringConstant(m, "built_for", BIND_TAG) < 0) Py_CLEAR(m);
+    return m;
+}

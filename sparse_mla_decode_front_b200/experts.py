@@ -29,15 +29,19 @@ _bound = None
 
 
 def _native():
-    """The native marshalling module, bound to the loaded library; raises if either is missing."""
+    """The native marshalling module, bound to the loaded library; raises if either is missing, or if
+    the module was built for another torch or Python (it reads tensors by their layout)."""
     global _bound
     if _bound is None:
         lib = _lib.lib()
+        fix = "build it with `python -m sparse_mla_decode_front_b200.build`"
         try:
             from . import _bind
         except ImportError as e:
-            raise ImportError("_bind.so is missing or does not fit this torch: build it with "
-                              "`python -m sparse_mla_decode_front_b200.build`") from e
+            raise ImportError(f"_bind.so is missing or cannot be loaded: {fix}") from e
+        built_for = getattr(_bind, "built_for", "an unknown torch")
+        if built_for != _lib.bind_tag():
+            raise ImportError(f"_bind.so was built for {built_for}, this is {_lib.bind_tag()}: {fix}")
         _bind.set_entries(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _ENTRIES])
         _bound = _bind
     return _bound

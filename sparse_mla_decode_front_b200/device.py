@@ -210,6 +210,9 @@ class ExpertLayer:
         self.normalize, self.scale, self.eps = normalize, scale, eps
         T, K, (held, hidden, width), n_experts = n_tokens, top_k, w_down.shape, router_weights.shape[1]
         rows, dev = T * K, w_down.device
+        self.device = dev
+        for name in ("gamma", "router_weights", "router_bias", "w_up", "w_up_scales", "w_down_scales"):
+            self._check_device(name, getattr(self, name))
         new = lambda *shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
         nbytes = api.mla_router_workspace_bytes(T, hidden, n_experts, K)
         if nbytes == 0:
@@ -228,8 +231,18 @@ class ExpertLayer:
         self.y, self.out = new(rows, hidden, dtype=bf16), new(T, hidden, dtype=bf16)
         self.status = torch.zeros(1, dtype=i32, device=dev)
 
+    def _check_device(self, name: str, t: Optional[torch.Tensor]) -> None:
+        if t is not None and t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the layer on {self.device}")
+
     def run(self, hidden_states: torch.Tensor, stream=None) -> torch.Tensor:
-        """``out`` [n_tokens, hidden] of ``hidden_states`` (bf16), enqueued on ``stream``."""
+        """``out`` [n_tokens, hidden] of ``hidden_states`` (bf16), enqueued on ``stream`` (None: torch's current
+        one of the layer's device, whichever device is current)."""
+        self._check_device("hidden_states", hidden_states)
+        with torch.cuda.device(self.device):
+            return self._run(hidden_states, stream)
+
+    def _run(self, hidden_states, stream):
         api.mla_rmsnorm_router_topk(hidden_states, self.gamma, self.router_weights, self.router_bias, self.eps,
                                     self.top_k, self.act, self.norm, self.topk_idx, self.affinities,
                                     self.router_workspace, stream)
@@ -246,4 +259,5 @@ class ExpertLayer:
 
     def device_status(self, stream=None) -> int:
         """Bits of the waits that gave up since the layer was made (0: none)."""
-        return api.mla_get_device_status(self.status, stream)
+        with torch.cuda.device(self.device):
+            return api.mla_get_device_status(self.status, stream)

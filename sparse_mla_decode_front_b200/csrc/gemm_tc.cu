@@ -174,10 +174,19 @@ bool make_tma_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t ou
     const cuuint32_t estride[2] = {1, 1};
     const CUtensorMapDataType type =
         element_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    if (fn(map, type, 2, const_cast<void*>(base), gdim, gstride, box, estride,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return false;
+    const auto encode = [&] {
+        return fn(map, type, 2, const_cast<void*>(base), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = encode();
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {
+        // This call of the driver wants a current context, which a host thread has only from its first
+        // runtime call that needs one on: make the thread's device current, as the launch would.
+        int dev = 0;
+        if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
+    }
+    if (r != CUDA_SUCCESS) return false;
     std::lock_guard<std::mutex> lock(c.mu);
     const int slot = c.used < kMapCache ? c.used++ : (c.next++ % kMapCache);
     c.key[slot] = k;

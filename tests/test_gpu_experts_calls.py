@@ -102,3 +102,84 @@ g.replay()
 torch.cuda.synchronize()
 assert np.array_equal(src.cpu().numpy(), np.argsort(idx.cpu().numpy().reshape(-1), kind="stable"))
 """)
+
+
+PRODUCTS = """
+import threading
+import torch
+from sparse_mla_decode_front_b200 import api, experts as G
+g = torch.Generator(device="cuda").manual_seed(1)
+e4m3 = lambda *s: (torch.randn(*s, generator=g, device="cuda") * 60).clamp(-448, 448).to(torch.float8_e4m3fn)
+blocks = lambda v: -(-v // 128)
+scales = lambda *s: torch.rand(*s, generator=g, device="cuda")
+
+
+def plain(m, n, k):
+    args = (e4m3(m, k), scales(blocks(k), m), e4m3(n, k), scales(blocks(n), blocks(k)))
+    return lambda out, stream=None: G.mla_fp8_matmul(*args, out, None, stream), (m, n)
+
+
+def grouped(rows, n, k):
+    m = 2 * rows
+    off = torch.tensor([0, rows, m], dtype=torch.int32, device="cuda")
+    args = (e4m3(m, k), scales(blocks(k), m), e4m3(2, n, k), scales(2, blocks(n), blocks(k)), off)
+    return lambda out, stream=None: G.mla_fp8_grouped_matmul(*args, out, None, stream), (m, n)
+
+
+def router(t, h):
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+    args = (rnd(t, h), rnd(h), rnd(h, 64))
+    return lambda out, stream=None: out.copy_(api.rmsnorm_router_topk(*args, top_k=4)[0]), (t, h)
+
+
+def in_threads(jobs, after=None):
+    errors = []
+
+    def work(call, out, stream):
+        try:
+            if after is not None:
+                after.wait()
+            call(out, stream)
+        except Exception as e:
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+
+
+def job(made):
+    return made[0], torch.zeros(made[1], device="cuda"), torch.cuda.Stream()
+"""
+
+
+def test_a_host_threads_first_call_of_cuda():
+    # the thread has no context yet, and nothing else in it has asked for one; inputs that no call saw
+    run_alone(PRODUCTS + """
+for make in (lambda: plain(1, 1536, 1024), lambda: plain(300, 512, 640), lambda: grouped(3, 144, 400),
+             lambda: grouped(300, 144, 400), lambda: router(5, 256)):
+    first = job(make())                          # this thread's call: what is kept for a device is known now
+    first[0](first[1])
+    call, out, _ = job(make())
+    torch.cuda.synchronize()
+    in_threads([(call, out, None)])
+    again = torch.zeros_like(out)
+    call(again)
+    assert torch.equal(out, again) and bool(out.any())
+""")
+
+
+def test_first_products_of_a_process_from_several_host_threads():
+    # each sees the same clusters per device, and so the same split and order of the sums
+    run_alone(PRODUCTS + """
+jobs = [job(plain(*s)) for s in [(1, 1536, 4096), (20, 144, 2064), (64, 2048, 1168), (300, 512, 640)] * 2]
+torch.cuda.synchronize()
+in_threads(jobs, threading.Barrier(len(jobs)))
+for call, out, _ in jobs:
+    again = torch.zeros_like(out)
+    call(again)
+    assert torch.equal(out, again) and bool(out.any())
+""")

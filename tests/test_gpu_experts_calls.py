@@ -4,7 +4,12 @@ import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
+import torch
+
+import test_gpu_experts as base
+from sparse_mla_decode_front_b200 import experts as G
 
 pytestmark = pytest.mark.gpu
 
@@ -183,3 +188,44 @@ for call, out, _ in jobs:
     call(again)
     assert torch.equal(out, again) and bool(out.any())
 """)
+
+
+# ------------------------------------------------------------------ grouped products
+def wrong_tables(R):
+    return [[0, 9 * R, 10 * R, 20 * R], [-5, R // 10, R // 5, R // 3], [R // 2, R // 10, R // 5, R], [R] * 4,
+            [0, 2 ** 31 - 1, -2 ** 31, 7], [R // 3, 0, 2 * R // 3, R // 2], [R, 0, 0, R], [-1, -2, -3, -4]]
+
+
+@pytest.mark.parametrize("table", range(8))
+@pytest.mark.parametrize("R", [24, 60, 100, 700])   # three groups: tiles of 16, 32 and 64 rows, and the many-rows form
+def test_grouped_matmul_of_a_wrong_table_gives_the_clamped_groups(R, table):
+    N, K = 272, 400
+    x, xs = base.make_operand(R, K, R)
+    w, ws = base.make_weight(3, N, K, 4)
+    buf, status = base.filled(R + 2, N, dtype=torch.float32), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, bad = buf[1:R + 1], wrong_tables(R)[table]
+    G.mla_fp8_grouped_matmul(x, xs, w, ws, torch.tensor(bad, dtype=torch.int32, device="cuda"), out, status)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    ends = np.maximum.accumulate(np.clip(np.array(bad, np.int64), 0, R))   # clamped, and to the running maximum
+    assert base.untouched(buf[0]) and base.untouched(buf[-1])
+    assert base.untouched(out[:ends[0]]) and base.untouched(out[ends[-1]:])
+    for e in range(3):
+        part = slice(int(ends[e]), int(ends[e + 1]))
+        if part.start < part.stop:
+            base.check_product(out[part], x[part], xs[:, part], w[e], ws[e], torch.float32, f"expert {e}")
+
+
+@pytest.mark.parametrize("N,K", [(16, 16), (272, 1040), (512, 256)])
+@pytest.mark.parametrize("name", ["decode", "uneven", "long"])
+def test_grouped_matmul_to_fp16(name, N, K):
+    counts = base.GROUPS[name]
+    ends = np.concatenate([[0], np.cumsum(counts)])
+    x, xs = base.make_operand(int(ends[-1]), K, K)
+    w, ws = base.make_weight(len(counts), N, K, N)
+    out = base.filled(int(ends[-1]), N, dtype=torch.float16)
+    G.mla_fp8_grouped_matmul(x, xs, w, ws, torch.tensor(ends, dtype=torch.int32, device="cuda"), out)
+    for e, c in enumerate(counts):
+        part = slice(ends[e], ends[e + 1])
+        if c:
+            base.check_product(out[part], x[part], xs[:, part], w[e], ws[e], torch.float16, f"expert {e}")

@@ -151,15 +151,22 @@ cudaError_t few_cost(const fp8::Problem& p, int dev, int block, long long* cost)
 // a pair's 256 x 256. The plain product's tiles are known, so the estimates are compared
 // (measured, us, few of 16 / 32 / 64 / 128 / many, K = 7168: 16 x 7168 15.6 / 16.3 / 17.3 / 21.1 /
 // 35.2, 128 x 1536 22 / 17 / 13.7 / 12.8 / 34.8, 256 x 7168 120 / 74 / 45 / 34.8 / 33.5,
-// 512 x 1536 55 / 40 / 25 / 27 / 33). Of groups only the rows' capacity is known, so it goes by
-// the average (32 experts, N = 4096, K = 7168: 8 rows 141 / 143 / 151 / 198 / 249, 32 rows
-// 355 / 222 / 197 / 244 / 251, 64 rows 544 / 353 / 220 / 243 / 252, 96 rows 799 / 471 / 293 / 286 / 253);
-// at 17 to 32 the narrower tile, since a rank that holds a share of the experts has fewer rows than
-// capacity (4 rows at a capacity of 32: 142 against 151).
+// 512 x 1536 55 / 40 / 25 / 27 / 33).
+// Of groups the host knows only the rows' capacity, so it goes by the capacity an expert, between what
+// three kinds of call want (32 experts, N = 4096, K = 7168, us, few of 16 / 32 / 64 / many):
+//   equal groups                8: 141 / 143 / 151 / 171, 32: 237 / 146 / 154 / 173, 48: 369 / 261 / 155 / 173,
+//                              64: 485 / 256 / 156 / 174, 96: 764 / 383 / 277 / 177
+//   a router's (largest 2.5 x)  8: 152 / 141 / 147 / 162, 32: 304 / 201 / 166 / 165, 48: 397 / 240 / 190 / 166,
+//                              64: 522 / 319 / 220 / 165, 96: 756 / 426 / 275 / 192
+//   a rank with an eighth       8: 80 / 82 / 87 / 93, 32: 111 / 114 / 120 / 123, 48: 124 / 121 / 126 / 134,
+//   of the experts             64: 142 / 133 / 140 / 148, 96: 162 / 143 / 146 / 160, 256: 289 / 202 / 167 / 163
+// The narrow tiles go as far as a rank with a share gains by them and the others lose little, 64 rows to a
+// capacity of 48. Past that many rows, which loses 12 % at most (a share's 96), while 64 rows lose 33 % at
+// a router's 64.
 cudaError_t choose(const fp8::Problem& p, int dev, int* width) {
     if (p.offsets) {
         const long long g = p.groups;
-        *width = p.rows <= 8 * g ? 16 : p.rows <= 32 * g ? 32 : p.rows <= 64 * g ? 64 : 0;
+        *width = p.rows <= 8 * g ? 16 : p.rows <= 32 * g ? 32 : p.rows <= 48 * g ? 64 : 0;
         return cudaSuccess;
     }
     const long long pairs = std::max(1, sms_of(dev) / 2);

@@ -229,3 +229,20 @@ def test_grouped_matmul_to_fp16(name, N, K):
         part = slice(ends[e], ends[e + 1])
         if c:
             base.check_product(out[part], x[part], xs[:, part], w[e], ws[e], torch.float16, f"expert {e}")
+
+
+@pytest.mark.parametrize("dtype", base.DT)
+@pytest.mark.parametrize("capacity", [8, 9, 32, 33, 48, 49])   # an expert: both sides of each change of form
+def test_grouped_matmul_where_the_form_changes(capacity, dtype):
+    E, N, K = 5, 144, 272
+    counts = [0, 2 * capacity, 1, 3 * capacity // 2, capacity // 2 - 1]
+    ends, R = np.concatenate([[0], np.cumsum(counts)]), E * capacity
+    x, xs = base.make_operand(R, K, capacity)
+    w, ws = base.make_weight(E, N, K, N)
+    out = base.filled(R, N, dtype=dtype)
+    G.mla_fp8_grouped_matmul(x, xs, w, ws, torch.tensor(ends, dtype=torch.int32, device="cuda"), out)
+    for e, c in enumerate(counts):
+        part = slice(ends[e], ends[e + 1])
+        if c:
+            base.check_product(out[part], x[part], xs[:, part], w[e], ws[e], dtype, f"expert {e}")
+    assert base.untouched(out[ends[-1]:])

@@ -88,7 +88,8 @@ int mla_moe_sort(const int32_t* topk_idx, const void* affinities, int n_tokens, 
  *   scales  [ceil(hidden / 128), n_rows] fp32 (quantised as mla_fp8_quantize does)
  *
  * Limits: hidden a positive multiple of 16, up to 2^30; 1 <= top_k <= 32; n_tokens and
- * n_rows >= 0, n_tokens * top_k <= 2^30, n_tokens * hidden < 2^42. */
+ * n_rows >= 0, n_tokens * top_k <= 2^30, n_tokens * hidden <= 2^42 - 2048 (hidden
+ * counted up to the next multiple of 512). */
 int mla_moe_gather(const void* x, int dtype, const int32_t* row_of, int n_tokens, int top_k, int hidden, int n_rows,
                    void* rows, float* scales, void* stream);
 
@@ -126,7 +127,8 @@ int mla_moe_combine_backward(const void* grad_out, const void* rows, int dtype, 
  *   q           [n_rows, cols] e4m3 (written)
  *   scales      [ceil(cols / 128), n_rows] fp32 (written)
  *
- * Limits: cols a positive multiple of 16; n_rows >= 0. */
+ * Limits: cols a positive multiple of 16, up to 2^29; n_rows >= 0, n_rows * cols <= 2^42 - 2048
+ * (cols counted up to the next multiple of 512). */
 int mla_fp8_quantize(const void* x, int dtype, int n_rows, int cols, int gated, const int32_t* valid_rows, void* q,
                      float* scales, void* stream);
 
@@ -142,8 +144,11 @@ int mla_fp8_quantize(const void* x, int dtype, int n_rows, int cols, int gated, 
  *             on-device wait gave up (the output is invalid then); never cleared by the call
  *             (read it with mla_get_device_status)
  *
- * Limits: n and k positive multiples of 16, up to 2^30; n_rows from 0 to 2^30, and n_rows * n
- * < 2^40. */
+ * A block's factor x_scales * w_scales is rounded to fp32 by itself, so it has to lie in fp32's
+ * range.
+ *
+ * Limits: n and k positive multiples of 16, up to 2^30; n_rows from 0 to 2^30, and
+ * (n_rows / 16 + 1) * ceil(n / 128) < 2^30. */
 int mla_fp8_matmul(const void* x, const float* x_scales, const void* w, const float* w_scales, int n_rows, int n,
                    int k, void* out, int out_dtype, int32_t* status, void* stream);
 
@@ -153,7 +158,8 @@ int mla_fp8_matmul(const void* x, const float* x_scales, const void* w, const fl
  *   w         [n_experts, n, k] e4m3, w_scales [n_experts, ceil(n / 128), ceil(k / 128)]
  *   expert_offsets  [n_experts + 1] int32 on the device
  *
- * Limits: as above; 1 <= n_experts <= 1024; n_experts * n < 2^31. */
+ * Limits: as above, with (n_rows / 16 + n_experts) * ceil(n / 128) < 2^30; 1 <= n_experts <= 1024;
+ * n_experts * n < 2^31. */
 int mla_fp8_grouped_matmul(const void* x, const float* x_scales, const void* w, const float* w_scales,
                            const int32_t* expert_offsets, int n_rows, int n_experts, int n, int k, void* out,
                            int out_dtype, int32_t* status, void* stream);

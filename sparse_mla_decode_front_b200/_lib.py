@@ -112,7 +112,6 @@ SIGNATURES.update({   # include/moe_experts.h
     "mla_fp8_matmul": (_I, [_VP] * 4 + [_I] * 3 + [_VP, _I, _VP, _VP]),
     "mla_fp8_grouped_matmul": (_I, [_VP] * 5 + [_I] * 4 + [_VP, _I, _VP, _VP]),
 })
-MLA_DTYPE_BF16, MLA_DTYPE_FP16, MLA_DTYPE_FP32 = 0, 1, 2
 MLA_ROUTER_SIGMOID = 0
 MLA_ROUTER_SOFTMAX = 1
 

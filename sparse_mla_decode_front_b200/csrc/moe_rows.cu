@@ -210,7 +210,7 @@ k_moe_combine(const T* rows, const int32_t* row_of, const float* weights, int n_
 // choices 3.4 / 4.2 / 4.5 / 6.6, 584 5.5 / 4.4 / 6.4 / 10.5, 1024 9.5 / 7.5 / 7.1 / 10.9, 2048 16.9 /
 // 13.0 / 12.2 / 11.8, 16384 138 / 98 / 89 / 84; rows of 1024: 1024 choices 6.2 / 3.8 / 2.6 / 2.8).
 constexpr int kBackWarps = 8;
-constexpr int kBackTeamWarps = 16 * 148;   // 16 an SM
+constexpr int kBackSmWarps = 16;
 template <class T>
 __global__ void __launch_bounds__(32 * kBackWarps)
 k_moe_combine_backward(const T* dout, const T* rows, const int32_t* row_of,
@@ -356,6 +356,12 @@ k_fp8_quantize(const T* x, int R, int C, int units, const int32_t* valid_rows, u
 int row_units(int width, bool whole_blocks) {
     return whole_blocks ? (width + kScaleBlock - 1) / kScaleBlock * kLanesPerScale : width / kUnit;
 }
+// SMs of the current device.
+cudaError_t count_sms(int* sms) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
 unsigned blocks_for(long long rows, int units) { return (unsigned)((rows * units + kThreads - 1) / kThreads); }
 
 template <class T>
@@ -382,8 +388,10 @@ cudaError_t combine_backward_as(const void* dout, const void* rows, const int32_
                                 int K, int H, int R, void* drows, float* dw, cudaStream_t s) {
     const long long n = (long long)T_ * K;
     const int units = row_units(H, false);
-    int team = kBackWarps;
-    while (team > 1 && n * team > kBackTeamWarps) team >>= 1;
+    int team = kBackWarps, sms = 0;
+    const cudaError_t e = count_sms(&sms);
+    if (e != cudaSuccess) return e;
+    while (team > 1 && n * team > (long long)kBackSmWarps * sms) team >>= 1;
     const long long per_block = kBackWarps / team;
     return launch_pdl(k_moe_combine_backward<T>, dim3((unsigned)((n + per_block - 1) / per_block)),
                       dim3(32 * kBackWarps), 0, s, static_cast<const T*>(dout), static_cast<const T*>(rows), row_of, w,
@@ -399,9 +407,8 @@ cudaError_t quantize_as(const void* x, int R, int C, const int32_t* valid, void*
     if (!valid)
         return launch_pdl(k_fp8_quantize<T, GATED, false>, dim3(blocks), dim3(kThreads), 0, s, xt, R, C, units, valid, qt,
                           scales);
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int sms = 0;
+    const cudaError_t e = count_sms(&sms);
     if (e != cudaSuccess) return e;
     return launch_pdl(k_fp8_quantize<T, GATED, true>, dim3(std::min(blocks, 16u * sms)), dim3(kThreads), 0, s, xt, R, C,
                       units, valid, qt, scales);

@@ -110,8 +110,8 @@ int mla_moe_combine(const void* rows, int dtype, const int32_t* row_of, const fl
  *   grad_weights[t, k]      = <grad_out[t], rows[row_of[t, k]]>, fp32; 0 for a choice without a row
  * row_of names a row at most once, as mla_moe_sort writes it (the gradients of a row named
  * twice are not added up; what grad_rows then holds there is not defined).
- * grad_rows or grad_weights may be NULL when it is not wanted (not both); weights may be
- * NULL (ones), and rows may be NULL when grad_weights is. */
+ * grad_rows or grad_weights may be NULL when it is not wanted (not both, unless n_rows is 0);
+ * weights may be NULL (ones), and rows may be NULL when grad_weights is. */
 int mla_moe_combine_backward(const void* grad_out, const void* rows, int dtype, const int32_t* row_of,
                              const float* weights, int n_tokens, int top_k, int hidden, int n_rows, void* grad_rows,
                              float* grad_weights, void* stream);

@@ -133,7 +133,8 @@ int mla_moe_combine_backward(const void* grad_out, const void* rows, int dtype, 
     if (n_tokens == 0) return MLA_OK;
     rc = check({grad_out}, {row_of});
     if (rc != MLA_OK) return rc;
-    if (!grad_weights && (!grad_rows || n_rows == 0)) return grad_rows ? MLA_OK : MLA_ERR_NULL_POINTER;
+    if (!grad_weights && n_rows == 0) return MLA_OK;   // nothing to write (an empty tensor's address is null)
+    if (!grad_weights && !grad_rows) return MLA_ERR_NULL_POINTER;
     if (grad_weights && !rows && n_rows > 0) return MLA_ERR_NULL_POINTER;
     if (misaligned(rows, 16) || misaligned(grad_rows, 16) || misaligned(weights, 4) || misaligned(grad_weights, 4))
         return MLA_ERR_MISALIGNED;

@@ -36,3 +36,12 @@ def test_products():
         == product(0, 1 << 21, E=1024) == _lib.MLA_ERR_UNSUPPORTED_DIMS
     # (rows / 16 + experts) * ceil(n / 128) reaches 2^30
     assert product(1 << 30, 2048) == product((1 << 24) - 16 * 512, 1 << 17, E=512) == _lib.MLA_ERR_UNSUPPORTED_DIMS
+
+
+def test_gradient_of_no_rows():
+    # an empty tensor has no address: with no rows there is no grad_rows to write, given or not
+    def back(R, grad_rows, grad_weights=None):
+        return _lib.lib().mla_moe_combine_backward(P[0], None, 0, P[1], P[2], 4, 2, 64, R, grad_rows, grad_weights,
+                                                   None)
+    assert back(0, P[3]) == back(0, None) == _lib.MLA_OK
+    assert back(8, None) == _lib.MLA_ERR_NULL_POINTER

@@ -246,3 +246,26 @@ def test_grouped_matmul_where_the_form_changes(capacity, dtype):
         if c:
             base.check_product(out[part], x[part], xs[:, part], w[e], ws[e], dtype, f"expert {e}")
     assert base.untouched(out[ends[-1]:])
+
+
+# ------------------------------------------------------------------ no rows, no tokens
+def test_movers_without_rows_or_tokens():
+    # a rank none of whose experts was taken, with buffers of no rows; and a call without tokens
+    T, K, H = 3, 2, 64
+    x = torch.randn(T, H, device="cuda").to(torch.bfloat16)
+    w, row_of = torch.rand(T, K, device="cuda"), torch.full((T, K), -1, dtype=torch.int32, device="cuda")
+    rows = torch.empty(0, H, dtype=torch.bfloat16, device="cuda")
+    out, gw = base.filled(T, H, dtype=torch.bfloat16), base.filled(T, K, dtype=torch.float32)
+    G.mla_moe_gather(x, row_of, rows)
+    G.mla_moe_gather(x, row_of, torch.empty(0, H, dtype=torch.uint8, device="cuda").view(base.E4M3),
+                     torch.empty(1, 0, device="cuda"))
+    G.mla_moe_combine(rows, row_of, w, out)
+    G.mla_moe_combine_backward(x, rows, row_of, w, torch.empty_like(rows), None)
+    G.mla_moe_combine_backward(x, None, row_of, w, torch.empty_like(rows), None)
+    G.mla_moe_combine_backward(x, rows, row_of, w, torch.empty_like(rows), gw)
+    assert not out.any() and not gw.any()
+    some = base.filled(4, H, dtype=torch.bfloat16)
+    G.mla_moe_gather(x[:0], row_of[:0], some)
+    G.mla_moe_combine(some, row_of[:0], w[:0], out[:0])
+    G.mla_moe_combine_backward(x[:0], some, row_of[:0], w[:0], some, gw[:0])
+    assert base.untouched(some)

@@ -145,7 +145,7 @@ struct MapCache {
     std::mutex mu;
     MapKey key[kMapCache];
     CUtensorMap map[kMapCache];
-    int used = 0, next = 0;
+    int used = 0, next = 0;   // next: the slot that is overwritten next once all are used
 };
 MapCache& map_cache() {
     static MapCache c;
@@ -188,7 +188,13 @@ bool make_tma_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t ou
     }
     if (r != CUDA_SUCCESS) return false;
     std::lock_guard<std::mutex> lock(c.mu);
-    const int slot = c.used < kMapCache ? c.used++ : (c.next++ % kMapCache);
+    int slot = c.used;
+    if (slot < kMapCache) {
+        ++c.used;
+    } else {
+        slot = c.next;
+        c.next = (slot + 1) % kMapCache;
+    }
     c.key[slot] = k;
     c.map[slot] = *map;
     return true;

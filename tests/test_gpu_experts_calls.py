@@ -248,6 +248,19 @@ def test_grouped_matmul_where_the_form_changes(capacity, dtype):
     assert base.untouched(out[ends[-1]:])
 
 
+def test_more_operands_than_kept_tensor_maps():
+    # every call's maps push out the oldest ones, several times round, and none is taken for another's
+    M, N, K, count = 5, 48, 144, 150
+    x, xs = base.make_operand(M, K, 1)
+    w, ws = base.make_weight(count, N, K, 2)
+    for _ in range(2):
+        out = base.filled(count, M, N, dtype=torch.float32)
+        for i in range(count):
+            G.mla_fp8_matmul(x, xs, w[i], ws[i], out[i])
+        for i in range(0, count, 7):
+            base.check_product(out[i], x, xs, w[i], ws[i], torch.float32, f"weight {i}")
+
+
 # ------------------------------------------------------------------ no rows, no tokens
 def test_movers_without_rows_or_tokens():
     # a rank none of whose experts was taken, with buffers of no rows; and a call without tokens

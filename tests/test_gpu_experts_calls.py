@@ -248,6 +248,31 @@ def test_grouped_matmul_where_the_form_changes(capacity, dtype):
     assert base.untouched(out[ends[-1]:])
 
 
+@pytest.mark.parametrize("rows", [1, 300])   # the few-rows form, and the many-rows one
+def test_weights_beyond_32_bits(rows):
+    E, N, K = 160, 4096, 7168                          # 4.7e9 bytes
+    held, part = [0, 74, 159], 32                      # the second lies past 2^31, the third past 2^32
+    w = torch.zeros(E, N, K, dtype=torch.uint8, device="cuda").view(base.E4M3)
+    ws = torch.ones(E, N // 128, K // 128, device="cuda")
+    for e in held:
+        one, scale = base.make_weight(1, N, K, e)
+        w.view(torch.uint8)[e], ws[e] = one[0].view(torch.uint8), scale[0]
+    counts = np.zeros(E, np.int64)
+    counts[held] = rows
+    if rows > 1:
+        counts[1:60] = 150                             # past 48 rows of capacity an expert
+    ends = np.concatenate([[0], np.cumsum(counts)])
+    x, xs = base.make_operand(int(ends[-1]), K, rows)
+    out = base.filled(int(ends[-1]), N, dtype=torch.float32)
+    G.mla_fp8_grouped_matmul(x, xs, w, ws, torch.tensor(ends, dtype=torch.int32, device="cuda"), out)
+    for e in held:
+        at = slice(int(ends[e]), int(ends[e + 1]))
+        for f in (0, N - part):                        # the first features and the last
+            base.check_product(out[at, f:f + part], x[at], xs[:, at], w[e, f:f + part], ws[e, f // 128:f // 128 + 1],
+                               torch.float32, f"expert {e}")
+    assert not out[int(ends[1]):int(ends[74])].any()
+
+
 def test_more_operands_than_kept_tensor_maps():
     # every call's maps push out the oldest ones, several times round, and none is taken for another's
     M, N, K, count = 5, 48, 144, 150

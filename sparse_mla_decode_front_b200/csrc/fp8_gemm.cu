@@ -162,7 +162,8 @@ cudaError_t few_cost(const fp8::Problem& p, int dev, int block, long long* cost)
 //   of the experts             64: 142 / 133 / 140 / 148, 96: 162 / 143 / 146 / 160, 256: 289 / 202 / 167 / 163
 // The narrow tiles go as far as a rank with a share gains by them and the others lose little, 64 rows to a
 // capacity of 48. Past that many rows, which loses 12 % at most (a share's 96), while 64 rows lose 33 % at
-// a router's 64.
+// a router's 64. (Short runs at 1.965 GHz; in a loop under the power cap, 64 / many, at 48 and 64: a
+// router's 213 / 208 and 256 / 216, a share's 173 / 190 and 179 / 195, equal groups 189 / 211 and 190 / 209.)
 cudaError_t choose(const fp8::Problem& p, int dev, int* width) {
     if (p.offsets) {
         const long long g = p.groups;
